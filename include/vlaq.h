@@ -7,7 +7,9 @@
  *   2. a block-scaled FP4 GEMM against offline NVFP4 weights, BF16 output,
  *      optional fused residual add;
  *   3. an FP8 E4M3 W8A8 variant (per-row weight scale, per-token activation
- *      scale).
+ *      scale);
+ *   4. FP8 with block scales of 128, and the residual update with its norms
+ *      between two blocks, fused with that quantization.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -302,6 +304,96 @@ VLAQ_API vlaq_status vlaq_linear_fp8(const uint8_t* xq, const float* s_x,
                             const void* residual, void* Y, int64_t M,
                             int64_t N, int64_t K, void* workspace,
                             size_t ws_bytes, void* stream);
+
+/* ----------------------------------------- FP8 with block scales of 128 */
+/* FP8 E4M3 with one fp32 scale per 128 values of a token row (activations)
+ * or per 128 x 128 block (weights), the granularity of block-quantized FP8
+ * checkpoints:
+ *   value = E4M3(code) * s,  s = max|v| / 448 over the block (correctly
+ *   rounded), code = E4M3_rne_sat(v / s) with v / s correctly rounded, zero
+ *   codes where s = 0.
+ * Codes are row-major [rows, K], one byte per element, as in the per-row
+ * variant.  Blocks start at multiples of 128; the last block of a row or
+ * column may be shorter (KB = ceil(K / 128), NB = ceil(N / 128)):
+ *   s_w  fp32 [NB, KB], row-major: block (n / 128, k / 128);
+ *   s_x  fp32 [KB, M]: block k / 128 of token m at (k / 128) * M + m (the
+ *        tokens of one block adjacent, as the linear's threads read them).
+ * Finite inputs only.
+ *
+ * RMSNorm in these entry points is the formula of VLAQ_F_RMSNORM with the
+ * sum of squares over 256 lanes instead of 32: lane l owns the 8-element
+ * chunks l, l + 256, ... in element order (fused multiply-add), an XOR
+ * butterfly 16, 8, 4, 2, 1 joins each 32 adjacent lanes and a butterfly
+ * 1, 2, 4 the eight groups.  A row's result depends on that row alone. */
+
+/* Offline weight quantization, 128 x 128 blocks.
+ *   W bf16 [N, K]; flags 0 or VLAQ_F_HADAMARD64 (rotate each row first);
+ *   codes out [N, K]; s_w out, fp32 [NB, KB].
+ * Limits: 1 <= N, 16 <= K <= 32768, K % 16 == 0. */
+VLAQ_API vlaq_status vlaq_quantize_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags,
+                                           uint8_t* codes, float* s_w, void* stream);
+
+/* Per-token activation quantization, 1 x 128 blocks, after the optional
+ * RMSNorm and rotation.
+ *   X bf16 [M, K]; gamma bf16 [K], required with VLAQ_F_RMSNORM, else
+ *   ignored; flags any of VLAQ_F_RMSNORM | VLAQ_F_HADAMARD64;
+ *   codes out [M, K]; s_x out, fp32 [KB, M].
+ * M == 0 is a no-op.  Limits: 16 <= K <= 32768, K % 16 == 0. */
+VLAQ_API vlaq_status vlaq_quantize_act_fp8_block(const void* X, int64_t M, int64_t K, const void* gamma, float eps,
+                                        uint32_t flags, uint8_t* codes, float* s_x, void* stream);
+
+/* Y[m, n] = bf16_rne( sum_b (s_x[b, m] * s_w[n / 128, b])
+ *                     * sum_{k in block b} e4m3(x)[m, k] e4m3(w)[n, k]
+ *                     + residual[m, n] )
+ * The sums inside a block are fp32 on the tensor cores (tcgen05
+ * kind::f8f6f4); the scaled sums of the blocks are added in fp32, in block
+ * order (within each of up to eight ranges of blocks, then over the ranges).
+ *   xq, s_x   activation codes [M, K] and scales [KB, M]
+ *   wq, s_w   weight codes [N, K] and scales [NB, KB]
+ *   residual  bf16 [M, N] or NULL; may be Y itself (in-place update)
+ *   Y         out, bf16 [M, N]
+ * No workspace: the CTAs that share a tile add their sums in shared memory.
+ * Calls may overlap on the GPU.  Every operand is read after the kernels
+ * launched before this call on the stream.  M == 0 is a no-op.  Limits:
+ * 1 <= N, N % 8 == 0, 16 <= K, K % 16 == 0. */
+VLAQ_API vlaq_status vlaq_linear_fp8_block(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                  const void* residual, void* Y, int64_t M, int64_t N, int64_t K, void* stream);
+
+/* ---------------------------------------------------------- residual norm */
+/* What runs between one block's output projection and the next block's
+ * input projection, in one pass over the row:
+ *   t  = RMSNorm(y) gamma_post      (y itself without gamma_post)
+ *   t  = t * gate[m / gate_rows]    (skipped without a gate)
+ *   c  = h + alpha * t              (every step one fp32 rounding)
+ *   H_out = bf16_rne(c)             the new residual stream
+ *   x  = RMSNorm(c) gamma_pre       from c before it is rounded to bf16
+ *   X_out = bf16_rne(x)
+ *   H, Y        bf16 [M, K]: residual stream and block output
+ *   gamma_post  bf16 [K] or NULL
+ *   gate        bf16 [ceil(M / gate_rows), K] or NULL: row m uses gate row
+ *               m / gate_rows, so gate_rows >= M is one learned vector (layer
+ *               scale), the padded sequence length one vector per sequence,
+ *               1 one per token; gate_rows >= 1 with a gate, else ignored
+ *   alpha       residual scale (host value, finite)
+ *   gamma_pre   bf16 [K]; may be NULL without X_out
+ *   H_out       out, bf16 [M, K]; may be H or Y itself (in-place update)
+ *   X_out       out, bf16 [M, K], or NULL (only the residual update); may be
+ *               Y itself unless H_out is.
+ * Both norms use eps and the 256-lane sum above.  Other buffers must not
+ * overlap the outputs.  M == 0 is a no-op.
+ * Limits: 16 <= K <= 32768, K % 16 == 0.  Finite inputs only. */
+VLAQ_API vlaq_status vlaq_residual_norm(const void* H, const void* Y, int64_t M, int64_t K, const void* gamma_post,
+                               const void* gate, int64_t gate_rows, float alpha, const void* gamma_pre,
+                               float eps, void* H_out, void* X_out, void* stream);
+
+/* The same with x quantized to FP8 with 1 x 128 block scales, optionally
+ * rotated first (flags 0 or VLAQ_F_HADAMARD64): codes out [M, K], s_x out
+ * fp32 [KB, M], the operands of vlaq_linear_fp8_block.  x is not rounded to
+ * bf16 on the way. */
+VLAQ_API vlaq_status vlaq_residual_norm_fp8_block(const void* H, const void* Y, int64_t M, int64_t K,
+                                         const void* gamma_post, const void* gate, int64_t gate_rows,
+                                         float alpha, const void* gamma_pre, float eps, uint32_t flags,
+                                         void* H_out, uint8_t* codes, float* s_x, void* stream);
 
 /* ----------------------------------------------------------- INT8 W8A8 */
 /* FoldQuant's 8-bit integer path ("FoldQuant W8A8/W4A4 inference and

@@ -69,6 +69,15 @@ def _load():
     lib.vo_quantize_fp8.argtypes = [P, i64, i64, P, ctypes.c_float, ctypes.c_uint, P, P]
     lib.vo_decode_fp8.restype = None
     lib.vo_decode_fp8.argtypes = [P, P, i64, i64, P]
+    lib.vo_sumsq_tree256.restype = ctypes.c_float
+    lib.vo_sumsq_tree256.argtypes = [P, i64]
+    lib.vo_quantize_fp8_block.restype = ctypes.c_int
+    lib.vo_quantize_fp8_block.argtypes = [P, i64, i64, P, ctypes.c_float, ctypes.c_uint, P, P]
+    lib.vo_quantize_weight_fp8_block.restype = ctypes.c_int
+    lib.vo_quantize_weight_fp8_block.argtypes = [P, i64, i64, ctypes.c_uint, P, P]
+    lib.vo_residual_norm.restype = ctypes.c_int
+    lib.vo_residual_norm.argtypes = [P, P, i64, i64, P, P, i64, ctypes.c_float, P, ctypes.c_float, ctypes.c_uint,
+                                     P, P, P, P]
     lib.vo_quantize_int8.restype = ctypes.c_int
     lib.vo_quantize_int8.argtypes = [P, i64, i64, P, ctypes.c_float, ctypes.c_uint, P, P]
     lib.vo_decode_int8.restype = None
@@ -235,6 +244,80 @@ def decode_fp8(codes, s) -> np.ndarray:
     out = np.empty((rows, K), dtype=np.float64)
     _load().vo_decode_fp8(_ptr(codes), _ptr(s), rows, K, _ptr(out))
     return out
+
+
+# ----------------------------------------------- FP8, block scales of 128
+def sumsq_tree256(x) -> np.float32:
+    x = _c(x, np.float32)
+    return np.float32(_load().vo_sumsq_tree256(_ptr(x), x.size))
+
+
+def quantize_fp8_block(X_bf16, gamma_bf16=None, eps=1e-6, flags=0):
+    """1 x 128 blocks: (codes u8 [rows, K], s f32 [KB, rows])."""
+    X = _c(X_bf16, np.uint16)
+    rows, K = X.shape
+    g_in = None if gamma_bf16 is None else _c(gamma_bf16, np.uint16)
+    codes = np.zeros((rows, K), dtype=np.uint8)
+    s = np.zeros(((K + 127) // 128, rows), dtype=np.float32)
+    rc = _load().vo_quantize_fp8_block(_ptr(X), rows, K, _ptr(g_in), ctypes.c_float(eps), flags, _ptr(codes), _ptr(s))
+    if rc != 0:
+        raise ValueError(f"oracle refused FP8 block quantization of K={K} flags={flags}")
+    return codes, s
+
+
+def quantize_weight_fp8_block(W_bf16, flags=0):
+    """128 x 128 blocks: (codes u8 [N, K], s f32 [NB, KB])."""
+    W = _c(W_bf16, np.uint16)
+    N, K = W.shape
+    codes = np.zeros((N, K), dtype=np.uint8)
+    s = np.zeros(((N + 127) // 128, (K + 127) // 128), dtype=np.float32)
+    rc = _load().vo_quantize_weight_fp8_block(_ptr(W), N, K, flags, _ptr(codes), _ptr(s))
+    if rc != 0:
+        raise ValueError(f"oracle refused FP8 block weight quantization of K={K} flags={flags}")
+    return codes, s
+
+
+_E4M3 = None
+
+
+def _e4m3_table():
+    global _E4M3
+    if _E4M3 is None:
+        _E4M3 = np.array([e4m3_decode(c) for c in range(256)])
+    return _E4M3
+
+
+def decode_fp8_block(codes, s) -> np.ndarray:
+    """fp64 values of 1 x 128 blocks (s [KB, rows])."""
+    K = codes.shape[1]
+    return _e4m3_table()[codes] * np.repeat(np.asarray(s, np.float64).T, 128, axis=1)[:, :K]
+
+
+def decode_weight_fp8_block(codes, s) -> np.ndarray:
+    """fp64 values of 128 x 128 blocks (s [NB, KB])."""
+    N, K = codes.shape
+    full = np.repeat(np.repeat(np.asarray(s, np.float64), 128, axis=0)[:N], 128, axis=1)[:, :K]
+    return _e4m3_table()[codes] * full
+
+
+def residual_norm(H, Y, gamma_post=None, gate=None, gate_rows=0, alpha=1.0, gamma_pre=None, eps=1e-6, flags=0,
+                  out="bf16"):
+    """bf16 bit patterns in; (h_out u16, x_out u16 or None) for out "bf16"
+    (None without gamma_pre), (h_out u16, codes u8, s f32 [KB, rows]) for
+    "fp8"."""
+    H, Y = _c(H, np.uint16), _c(Y, np.uint16)
+    rows, K = H.shape
+    opt = [None if t is None else _c(t, np.uint16) for t in (gamma_post, gate, gamma_pre)]
+    h = np.zeros((rows, K), dtype=np.uint16)
+    x = np.zeros((rows, K), dtype=np.uint16) if out == "bf16" and gamma_pre is not None else None
+    codes = np.zeros((rows, K), dtype=np.uint8) if out == "fp8" else None
+    s = np.zeros(((K + 127) // 128, rows), dtype=np.float32) if out == "fp8" else None
+    rc = _load().vo_residual_norm(_ptr(H), _ptr(Y), rows, K, _ptr(opt[0]), _ptr(opt[1]), max(gate_rows, 1),
+                                  ctypes.c_float(alpha), _ptr(opt[2]), ctypes.c_float(eps), flags, _ptr(h), _ptr(x),
+                                  _ptr(codes), _ptr(s))
+    if rc != 0:
+        raise ValueError(f"oracle refused the residual norm of K={K} flags={flags}")
+    return (h, x) if out == "bf16" else (h, codes, s)
 
 
 # -------------------------------------------------------------------- INT8

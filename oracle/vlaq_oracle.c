@@ -400,6 +400,145 @@ void vo_decode_fp8(const uint8_t* codes, const float* s, int64_t rows,
       out[r * K + k] = vo_e4m3_decode(codes[r * K + k]) * (double)s[r];
 }
 
+/* --------------------------------------- FP8 with block scales of 128 -- */
+/*
+ * One scale per 1 x 128 block of a row (s [KB, rows]) or per 128 x 128 block
+ * of a weight (s [NB, KB]): s = max|y| / 448 over the block (fp32), code =
+ * E4M3(y / s) (RNE, saturate), or 0 when s == 0.
+ *
+ * RMSNorm here sums squares over 256 lanes: lane l owns the 8-element chunks
+ * l, l + 256, ... in element order with a fused multiply-add, an XOR
+ * butterfly 16, 8, 4, 2, 1 joins each 32 adjacent lanes, a butterfly 1, 2, 4
+ * the eight groups.
+ */
+float vo_sumsq_tree256(const float* x, int64_t K) {
+  float lane[256], group[8];
+  int64_t nchunk = K / 8;
+  for (int l = 0; l < 256; ++l) {
+    float acc = 0.0f;
+    for (int64_t c = l; c < nchunk; c += 256)
+      for (int e = 0; e < 8; ++e) acc = fmaf(x[8 * c + e], x[8 * c + e], acc);
+    lane[l] = acc;
+  }
+  for (int g = 0; g < 8; ++g) {
+    float a[32];
+    memcpy(a, lane + 32 * g, sizeof a);
+    for (int off = 16; off >= 1; off >>= 1) {
+      float nxt[32];
+      for (int l = 0; l < 32; ++l) nxt[l] = a[l] + a[l ^ off];
+      memcpy(a, nxt, sizeof a);
+    }
+    group[g] = a[0];
+  }
+  for (int off = 1; off <= 4; off <<= 1) {
+    float nxt[8];
+    for (int g = 0; g < 8; ++g) nxt[g] = group[g] + group[g ^ off];
+    memcpy(group, nxt, sizeof group);
+  }
+  return group[0];
+}
+
+static void rmsnorm256_row(float* y, int64_t K, const uint16_t* gamma, float eps) {
+  float mean = vo_sumsq_tree256(y, K) / (float)K;
+  float v = mean + eps;
+  float r = 1.0f / sqrtf(v);
+  for (int64_t k = 0; k < K; ++k) y[k] = (y[k] * r) * vo_bf16_to_f32(gamma[k]);
+}
+
+static void fp8_blocks_row(const float* y, int64_t K, int64_t row, int64_t rows, uint8_t* codes, float* s) {
+  for (int64_t b = 0; b * 128 < K; ++b) {
+    int64_t k1 = (b + 1) * 128 < K ? (b + 1) * 128 : K;
+    float A = 0.0f;
+    for (int64_t k = b * 128; k < k1; ++k) A = fmaxf(A, fabsf(y[k]));
+    float sb = A / 448.0f;
+    s[b * rows + row] = sb;
+    for (int64_t k = b * 128; k < k1; ++k) codes[row * K + k] = (sb == 0.0f) ? 0 : vo_e4m3_encode(y[k] / sb);
+  }
+}
+
+int vo_quantize_fp8_block(const uint16_t* X, int64_t rows, int64_t K, const uint16_t* gamma, float eps,
+                          unsigned flags, uint8_t* codes, float* s) {
+  if (K <= 0 || K % 16 != 0) return -1;
+  if ((flags & VO_F_HADAMARD64) && K % 64 != 0) return -1;
+  if ((flags & VO_F_RMSNORM) && gamma == NULL) return -1;
+#pragma omp parallel for schedule(static)
+  for (int64_t r = 0; r < rows; ++r) {
+    float* y = (float*)malloc(sizeof(float) * (size_t)K);
+    for (int64_t k = 0; k < K; ++k) y[k] = vo_bf16_to_f32(X[r * K + k]);
+    if (flags & VO_F_RMSNORM) rmsnorm256_row(y, K, gamma, eps);
+    if (flags & VO_F_HADAMARD64) vo_wht64_inplace(y, K);
+    fp8_blocks_row(y, K, r, rows, codes, s);
+    free(y);
+  }
+  return 0;
+}
+
+int vo_quantize_weight_fp8_block(const uint16_t* W, int64_t N, int64_t K, unsigned flags, uint8_t* codes, float* s) {
+  if (K <= 0 || K % 16 != 0) return -1;
+  if ((flags & VO_F_HADAMARD64) && K % 64 != 0) return -1;
+  const int64_t kb = (K + 127) / 128;
+#pragma omp parallel for schedule(static)
+  for (int64_t n0 = 0; n0 < N; n0 += 128) {
+    const int64_t n1 = n0 + 128 < N ? n0 + 128 : N;
+    float* y = (float*)malloc(sizeof(float) * (size_t)(K * (n1 - n0)));
+    for (int64_t n = n0; n < n1; ++n) {
+      for (int64_t k = 0; k < K; ++k) y[(n - n0) * K + k] = vo_bf16_to_f32(W[n * K + k]);
+      if (flags & VO_F_HADAMARD64) vo_wht64_inplace(y + (n - n0) * K, K);
+    }
+    for (int64_t b = 0; b < kb; ++b) {
+      int64_t k1 = (b + 1) * 128 < K ? (b + 1) * 128 : K;
+      float A = 0.0f;
+      for (int64_t n = 0; n < n1 - n0; ++n)
+        for (int64_t k = b * 128; k < k1; ++k) A = fmaxf(A, fabsf(y[n * K + k]));
+      float sb = A / 448.0f;
+      s[(n0 / 128) * kb + b] = sb;
+      for (int64_t n = 0; n < n1 - n0; ++n)
+        for (int64_t k = b * 128; k < k1; ++k)
+          codes[(n0 + n) * K + k] = (sb == 0.0f) ? 0 : vo_e4m3_encode(y[n * K + k] / sb);
+    }
+    free(y);
+  }
+  return 0;
+}
+
+static uint16_t f32_to_bf16_rne(float v);
+
+/*
+ * Residual update with its norms, one fp32 rounding per step:
+ *   t = RMSNorm(y) gamma_post (y when gamma_post is NULL), t *= gate[m /
+ *   gate_rows] (unless NULL), c = h + alpha t, h_out = bf16(c), x =
+ *   RMSNorm(c) gamma_pre; x_out = bf16(x) and / or x (rotated with
+ *   VO_F_HADAMARD64) in FP8 blocks.  x_out or codes may be NULL.
+ */
+int vo_residual_norm(const uint16_t* H, const uint16_t* Y, int64_t rows, int64_t K, const uint16_t* gamma_post,
+                     const uint16_t* gate, int64_t gate_rows, float alpha, const uint16_t* gamma_pre, float eps,
+                     unsigned flags, uint16_t* h_out, uint16_t* x_out, uint8_t* codes, float* s) {
+  if (K <= 0 || K % 16 != 0) return -1;
+  if ((flags & VO_F_HADAMARD64) && K % 64 != 0) return -1;
+#pragma omp parallel for schedule(static)
+  for (int64_t r = 0; r < rows; ++r) {
+    float* c = (float*)malloc(sizeof(float) * (size_t)K);
+    for (int64_t k = 0; k < K; ++k) c[k] = vo_bf16_to_f32(Y[r * K + k]);
+    if (gamma_post) rmsnorm256_row(c, K, gamma_post, eps);
+    if (gate)
+      for (int64_t k = 0; k < K; ++k) c[k] = c[k] * vo_bf16_to_f32(gate[(r / gate_rows) * K + k]);
+    for (int64_t k = 0; k < K; ++k) {
+      float a = c[k] * alpha;
+      c[k] = vo_bf16_to_f32(H[r * K + k]) + a;
+      h_out[r * K + k] = f32_to_bf16_rne(c[k]);
+    }
+    if (x_out || codes) rmsnorm256_row(c, K, gamma_pre, eps);
+    if (x_out)
+      for (int64_t k = 0; k < K; ++k) x_out[r * K + k] = f32_to_bf16_rne(c[k]);
+    if (codes) {
+      if (flags & VO_F_HADAMARD64) vo_wht64_inplace(c, K);
+      fp8_blocks_row(c, K, r, rows, codes, s);
+    }
+    free(c);
+  }
+  return 0;
+}
+
 /* ---------------------------------------------------------------- INT8 -- */
 /*
  * INT8 symmetric per-row quantization ("FoldQuant W8A8/W4A4 inference ...":

@@ -1,0 +1,399 @@
+"""GPU parity of the FP8 block-128 linear, its quantizers and the residual
+norm.  Quantizers and the residual norm equal the oracle bit for bit; the
+linear is held to the fp64 product of the decoded operands by the element-wise
+bound of gpu_helpers.elementwise_bound (its accumulation chain, 128 sums inside
+a block, a product of scales, one fused multiply-add per block and at most
+seven sums over the K ranges, has fewer than K + 4 roundings)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import synthetic_inputs as si
+from gpu_helpers import bits, elementwise_bound, residual_f64, to_dev, vq
+
+pytestmark = pytest.mark.gpu
+
+RMS, HAD = 1, 2
+NAN = float("nan")
+
+
+def _same(a, b, what):
+    a, b = np.asarray(a), np.asarray(b)
+    if a.dtype == np.float32:
+        a, b = a.view(np.uint32), b.view(np.uint32)
+    bad = np.argwhere(a != b)
+    assert a.shape == b.shape and bad.size == 0, f"{what}: {len(bad)} differ, first {bad[:4].tolist()}"
+
+
+def _bf16_bits(t):
+    return t.cpu().view(torch.int16).numpy().view(np.uint16)
+
+
+def _check_gemm(Y, Y64, dx, dw, K, residual, what):
+    """The element-wise bound alone.  The relative Frobenius gate of 2e-3 that
+    large outputs meet does not follow from it for a few outputs: a bf16
+    rounding is off by up to 2^-8 of its value, so the Frobenius error of
+    correctly rounded outputs may reach 2^-8 = 3.9e-3; over N outputs with
+    independent errors it nears 1.7e-3."""
+    Y = Y.astype(np.float64)
+    assert np.isfinite(Y).all(), what
+    ratio = np.abs(Y - Y64) / elementwise_bound(Y64, Y, np.abs(dx) @ np.abs(dw).T, K, residual)
+    assert ratio.max() <= 1.0, (what, float(ratio.max()), np.unravel_index(int(ratio.argmax()), ratio.shape))
+
+
+# ---------------------------------------------------------------- quantizers
+def _act(X, gamma=None, flags=0):
+    m = vq()
+    M, K = X.shape
+    codes, s = m.alloc_fp8_block(M, K)
+    s.fill_(NAN)
+    m.vlaq_quantize_act_fp8_block(X.cuda(), M, K, None if gamma is None else gamma.cuda(), 1e-6, flags, codes, s)
+    torch.cuda.synchronize()
+    return codes.cpu().numpy(), s.cpu().numpy()
+
+
+# one block; partial blocks; one row; more blocks than a CTA's round; the
+# limits of each row length's kernel; several rows per block of threads
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 128), (5, 144), (1, 3584), (70, 336), (130, 1040), (4, 2048), (3, 2064),
+                                 (2, 4096), (3, 4112), (2, 8192), (2, 8208), (3, 18944), (1, 32768), (9500, 64)])
+@pytest.mark.parametrize("flags", [0, RMS, HAD, RMS | HAD])
+def test_act_blocks_equal_the_oracle(M, K, flags):
+    if flags & HAD and K % 64:
+        K = (K + 63) // 64 * 64
+        if K > 32768:
+            pytest.skip("past the limit")
+    X = si.projection_activations(K, M, 21)
+    gam = si.norm_gain(K, 21)
+    ref = oracle.quantize_fp8_block(bits(X), bits(gam), 1e-6, flags)
+    got = _act(X, gam, flags)
+    _same(got[1], ref[1], "scales")
+    _same(got[0], ref[0], "codes")
+
+
+def test_act_blocks_edge_values():
+    """Zero blocks, a single non-zero, the smallest bf16 subnormal, the
+    largest finite bf16, negative zeros."""
+    X = torch.zeros(6, 400, dtype=torch.bfloat16)
+    X[1, 399] = -3.0
+    X[2, :128] = torch.tensor(2.0 ** -133)
+    X[2, 5] = -(2.0 ** -130)
+    X[3] = torch.finfo(torch.bfloat16).max
+    X[3, 7] = -1.0
+    X[4] = -0.0
+    X[4, 200] = 1.0
+    X[5, ::3] = 2.0 ** -70
+    ref = oracle.quantize_fp8_block(bits(X))
+    got = _act(X)
+    _same(got[1], ref[1], "scales")
+    _same(got[0], ref[0], "codes")
+
+
+def test_act_row_does_not_depend_on_the_batch():
+    X = si.projection_activations(3584, 257, 4)
+    gam = si.norm_gain(3584, 4)
+    for flags in (0, RMS, RMS | HAD):
+        all_c, all_s = _act(X, gam, flags)
+        for r in (0, 128, 256):
+            c, s = _act(X[r:r + 1], gam, flags)
+            _same(c[0], all_c[r], "codes")
+            _same(s[:, 0], np.ascontiguousarray(all_s[:, r]), "scales")
+
+
+@pytest.mark.parametrize("N,K", [(1, 16), (8, 128), (127, 144), (129, 336), (264, 3584), (3, 32768), (1000, 1040)])
+@pytest.mark.parametrize("flags", [0, HAD])
+def test_weight_blocks_equal_the_oracle(N, K, flags):
+    m = vq()
+    if flags:
+        K = (K + 63) // 64 * 64
+    W = si.projection_weight(K, N, 9)
+    W[0] = 0
+    ref = oracle.quantize_weight_fp8_block(bits(W), flags)
+    codes, s = m.alloc_fp8_block(N, K, weight=True)
+    m.vlaq_quantize_weight_fp8_block(W.cuda(), N, K, flags, codes, s)
+    _same(s.cpu().numpy(), ref[1], "scales")
+    _same(codes.cpu().numpy(), ref[0], "codes")
+
+
+# ------------------------------------------------------------- residual norm
+def _norm_case(M, K, post, gate_rows, seed=33):
+    h, y = si.projection_activations(K, M, seed), si.projection_activations(K, M, seed + 1)
+    gp = si.norm_gain(K, seed) if post else None
+    g = si.norm_gain(K, seed + 1)
+    gate = si.projection_activations(K, -(-M // gate_rows), seed + 2) if gate_rows else None
+    return h, y, gp, g, gate
+
+
+def _dev(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def _b(t):
+    return None if t is None else bits(t)
+
+
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 144), (7, 3584), (300, 336), (2, 2048), (5, 4112), (3, 8192), (2, 18944),
+                                 (1, 32768), (9500, 64)])
+@pytest.mark.parametrize("post,gate,alpha", [(True, "none", 1.0), (False, "token", 0.5), (True, "vector", 0.22),
+                                             (False, "none", -1.5), (True, "group", 1.0)])
+def test_residual_norm_equals_the_oracle(M, K, post, gate, alpha):
+    m = vq()
+    gate_rows = {"none": 0, "token": 1, "vector": M + 5, "group": (M + 2) // 3}[gate]
+    h, y, gp, g, gt = _norm_case(M, K, post, gate_rows)
+    ho, xo = oracle.residual_norm(_b(h), _b(y), _b(gp), _b(gt), gate_rows, alpha, _b(g))
+    hd, yd, gpd, gd, gtd = _dev(h, y, gp, g, gt)
+    H = torch.full((M, K), NAN, dtype=torch.bfloat16, device="cuda")
+    X = torch.full_like(H, NAN)
+    m.vlaq_residual_norm(hd, yd, M, K, gpd, gtd, gate_rows, alpha, gd, 1e-6, H, X)
+    _same(_bf16_bits(H), ho, "h")
+    _same(_bf16_bits(X), xo, "x")
+    # only the update
+    m.vlaq_residual_norm(hd, yd, M, K, gpd, gtd, gate_rows, alpha, None, 1e-6, H.zero_(), None)
+    _same(_bf16_bits(H), ho, "h without x")
+    for flags in (0, HAD) if K % 64 == 0 else (0,):
+        ref = oracle.residual_norm(_b(h), _b(y), _b(gp), _b(gt), gate_rows, alpha, _b(g), 1e-6, flags, "fp8")
+        codes, s = m.alloc_fp8_block(M, K)
+        h2 = hd.clone()
+        m.vlaq_residual_norm_fp8_block(h2, yd, M, K, gpd, gtd, gate_rows, alpha, gd, 1e-6, flags, h2, codes, s)
+        _same(_bf16_bits(h2), ref[0], "h in place")
+        _same(s.cpu().numpy(), ref[2], "scales")
+        _same(codes.cpu().numpy(), ref[1], "codes")
+    h2, y2 = hd.clone(), yd.clone()
+    m.vlaq_residual_norm(h2, y2, M, K, gpd, gtd, gate_rows, alpha, gd, 1e-6, h2, y2)
+    _same(_bf16_bits(h2), ho, "h in place")
+    _same(_bf16_bits(y2), xo, "x over y")
+
+
+def test_residual_norm_of_zero_rows_is_finite():
+    """A row that cancels (c = 0) has x = 0 and zero scales, as eps > 0."""
+    m = vq()
+    M, K = 3, 272
+    h = si.projection_activations(K, M, 3).cuda()
+    codes, s = m.alloc_fp8_block(M, K)
+    H = torch.empty_like(h)
+    g = si.norm_gain(K, 3).cuda()
+    m.vlaq_residual_norm_fp8_block(h, h, M, K, None, None, 0, -1.0, g, 1e-6, 0, H, codes, s)
+    assert not H.float().any() and not s.any() and not (codes & 0x7F).any()
+
+
+# -------------------------------------------------------------------- linear
+def _linear_case(M, N, K, seed, residual):
+    X, W = si.projection_activations(K, M, seed), si.projection_weight(K, N, seed)
+    cx, sx = oracle.quantize_fp8_block(bits(X))
+    cw, sw = oracle.quantize_weight_fp8_block(bits(W))
+    R = si.residual(M, N, seed) if residual else None
+    dx, dw = oracle.decode_fp8_block(cx, sx), oracle.decode_weight_fp8_block(cw, sw)
+    return (cx, sx, cw, sw), R, dx, dw
+
+
+def _check_linear(M, N, K, residual, seed=31, rows=None):
+    m = vq()
+    ops, R, dx, dw = _linear_case(M, N, K, seed, residual)
+    d = [to_dev(t) for t in ops]
+    guard = 8
+    Y = torch.full((M + guard, N), NAN, dtype=torch.bfloat16, device="cuda")
+    Rd = None if R is None else R.cuda()
+    m.vlaq_linear_fp8_block(*d, Rd, Y, M, N, K)
+    torch.cuda.synchronize()
+    m.vlaq_check()
+    assert torch.isnan(Y[M:]).all(), "rows behind the last were written"
+    rows = np.arange(M) if rows is None else rows
+    Y64 = oracle.linear_f64(dx[rows], dw, None if R is None else bits(R)[rows])
+    _check_gemm(Y[:M].float().cpu().numpy()[rows], Y64, dx[rows], dw, K, residual_f64(R, rows),
+               f"fp8 block M={M} N={N} K={K} res={residual}")
+    if residual:
+        m.vlaq_linear_fp8_block(*d, Rd, Rd, M, N, K)
+        assert torch.equal(Rd, Y[:M]), "in-place residual"
+    else:
+        Y2 = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        m.vlaq_linear_fp8_block(*d, None, Y2, M, N, K)
+        assert torch.equal(Y2, Y[:M]), "two runs differ"
+
+
+# token counts at the borders of the column tiles; widths below, at and past a
+# weight block; depths of one partial block to many; every cluster size
+@pytest.mark.parametrize("M,N,K", [(1, 8, 16), (1, 128, 128), (1, 4608, 3584), (2, 136, 144), (16, 264, 1040),
+                                   (17, 128, 2048), (32, 120, 256), (33, 1000, 400), (64, 512, 3584), (65, 136, 272),
+                                   (128, 392, 1168), (129, 264, 3584), (8, 3584, 2064), (5, 8, 32), (300, 392, 1024),
+                                   (257, 3584, 512), (333, 1000, 1040)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_linear_equals_the_fp64_product(M, N, K, residual):
+    _check_linear(M, N, K, residual)
+
+
+# CTA pairs: one tile per pair, several per pair with an odd count, ragged
+# rows / columns / depth, and fewer blocks than pipeline stages
+@pytest.mark.parametrize("M,N,K", [(1024, 2560, 1024), (1000, 2600, 1040), (2048, 3328, 272), (700, 3336, 16),
+                                   (1030, 4616, 400), (2300, 4104, 128)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_linear_over_cta_pairs_equals_the_fp64_product(M, N, K, residual):
+    rng = np.random.default_rng(M)
+    rows = np.unique(np.concatenate([rng.choice(M, 60, replace=False), [0, M - 1]]))
+    _check_linear(M, N, K, residual, rows=rows)
+
+
+@pytest.mark.parametrize("M", [1, 40, 1024])
+def test_linear_scales_land_on_their_blocks(M):
+    """Codes of one and power-of-two scales, all different per block: each
+    output is an exact sum, so any block scaled by a neighbour's scale shows."""
+    m = vq()
+    N, K = 2560, 656
+    kb, nb = 6, 20
+    one = 0x38  # E4M3 1.0
+    cx = torch.zeros(M, K, dtype=torch.uint8, device="cuda")
+    cx[:, ::128] = one
+    cw = torch.full((N, K), one, dtype=torch.uint8, device="cuda")
+    e = torch.arange(M) % 5
+    sx = torch.stack([2.0 ** (e - b).float() for b in range(kb)]).cuda()
+    sw = (2.0 ** (torch.arange(nb)[:, None] % 4 - 2 * torch.arange(kb)[None, :] % 3).float()).cuda()
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    m.vlaq_linear_fp8_block(cx, sx, cw, sw, None, Y, M, N, K)
+    want = (sx.double().t() @ sw.double().t()).repeat_interleave(128, 1)
+    assert torch.equal(Y, want.to(torch.bfloat16))
+
+
+def test_linear_against_quantized_bf16_product():
+    """Block scales keep outlier channels apart: against the unquantized
+    product the error is the two operands' E4M3 rounding, at most half a step
+    (2^-4 relative) each, so 2^-4 + 2^-4 + 2^-8 of sum |x w| bounds it."""
+    m = vq()
+    M, N, K = 48, 384, 1024
+    X, W = si.projection_activations(K, M, 8), si.projection_weight(K, N, 8)
+    xq, sx = m.alloc_fp8_block(M, K)
+    wq, sw = m.alloc_fp8_block(N, K, weight=True)
+    m.vlaq_quantize_weight_fp8_block(W.cuda(), N, K, 0, wq, sw)
+    m.vlaq_quantize_act_fp8_block(X.cuda(), M, K, None, 1e-6, 0, xq, sx)
+    Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    m.vlaq_linear_fp8_block(xq, sx, wq, sw, None, Y, M, N, K)
+    x, w = X.double(), W.double()
+    exact, mass = x @ w.t(), x.abs() @ w.abs().t()
+    # below 2^-6 of the scale the step is absolute: 2^-10 s per element
+    floor = (sx.double().cpu().t().repeat_interleave(128, 1) * 2.0 ** -10) @ w.abs().t() \
+        + x.abs() @ (sw.double().cpu().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1) * 2.0 ** -10).t()
+    tol = (2.0 ** -3 + 2.0 ** -8 + 2.0 ** -8) * mass + 2 * floor + exact.abs() * 2.0 ** -8
+    assert ((Y.double().cpu() - exact).abs() <= tol).all()
+
+
+# ----------------------------------------------------------- used together
+def _block_chain(m, st):
+    """o projection -> residual norm -> gate_up -> down -> residual norm, as a
+    decoder layer runs them (the activation function left out)."""
+    M, K, F = st["M"], st["K"], st["F"]
+    m.vlaq_quantize_act_fp8_block(st["a"], M, K, None, 1e-6, 0, st["aq"], st["as"])
+    m.vlaq_linear_fp8_block(st["aq"], st["as"], st["wo"], st["so"], None, st["o"], M, K, K)
+    m.vlaq_residual_norm_fp8_block(st["h"], st["o"], M, K, st["g1"], None, 0, 1.0, st["g2"], 1e-6, 0, st["h1"],
+                                   st["xq"], st["xs"])
+    m.vlaq_linear_fp8_block(st["xq"], st["xs"], st["wu"], st["su"], None, st["u"], M, F, K)
+    m.vlaq_quantize_act_fp8_block(st["u"], M, F, None, 1e-6, 0, st["uq"], st["us"])
+    m.vlaq_linear_fp8_block(st["uq"], st["us"], st["wd"], st["sd"], None, st["d"], M, K, F)
+    m.vlaq_residual_norm(st["h1"], st["d"], M, K, st["g1"], None, 0, 1.0, st["g2"], 1e-6, st["h2"], st["x2"])
+
+
+def _chain_state(m, M, K, F, seed):
+    st = dict(M=M, K=K, F=F)
+    c = torch.device("cuda")
+    for name, n, k, i in (("o", K, K, 0), ("u", F, K, 1), ("d", K, F, 2)):
+        st["w" + name], st["s" + name] = m.alloc_fp8_block(n, k, weight=True)
+        m.vlaq_quantize_weight_fp8_block(si.projection_weight(k, n, seed + i).cuda(), n, k, 0, st["w" + name],
+                                         st["s" + name])
+    st["a"], st["h"] = si.projection_activations(K, M, seed).cuda(), si.projection_activations(K, M, seed + 1).cuda()
+    st["g1"], st["g2"] = si.norm_gain(K, seed).cuda(), si.norm_gain(K, seed + 1).cuda()
+    st["aq"], st["as"] = m.alloc_fp8_block(M, K)
+    st["xq"], st["xs"] = m.alloc_fp8_block(M, K)
+    st["uq"], st["us"] = m.alloc_fp8_block(M, F)
+    for n, w in (("o", K), ("u", F), ("d", K), ("h1", K), ("h2", K), ("x2", K)):
+        st[n] = torch.empty(M, w, dtype=torch.bfloat16, device=c)
+    return st
+
+
+@pytest.mark.parametrize("M,K,F", [(1, 512, 1360), (20, 512, 1360), (300, 1024, 4240)])
+def test_chain_equals_its_steps_from_the_oracle(M, K, F):
+    """Every step of the chain from the bytes the step before it left: the
+    quantizers and norms bit for bit, the linears within their bound."""
+    m = vq()
+    st = _chain_state(m, M, K, F, 61)
+    _block_chain(m, st)
+    torch.cuda.synchronize()
+    m.vlaq_check()
+    n = {k: (_bf16_bits(v) if isinstance(v, torch.Tensor) and v.dtype == torch.bfloat16
+             else v.cpu().numpy() if isinstance(v, torch.Tensor) else v) for k, v in st.items()}
+
+    def lin(xq, xs, wq, ws, y, k):
+        dx, dw = oracle.decode_fp8_block(n[xq], n[xs]), oracle.decode_weight_fp8_block(n[wq], n[ws])
+        _check_gemm(st[y].float().cpu().numpy(), oracle.linear_f64(dx, dw), dx, dw, k, None, f"chain {y} M={M}")
+
+    aq, s = oracle.quantize_fp8_block(n["a"])
+    _same(n["aq"], aq, "a codes"), _same(n["as"], s, "a scales")
+    lin("aq", "as", "wo", "so", "o", K)
+    h1, xq, xs = oracle.residual_norm(n["h"], n["o"], n["g1"], None, 0, 1.0, n["g2"], 1e-6, 0, "fp8")
+    _same(n["h1"], h1, "h1"), _same(n["xq"], xq, "x codes"), _same(n["xs"], xs, "x scales")
+    lin("xq", "xs", "wu", "su", "u", K)
+    uq, us = oracle.quantize_fp8_block(n["u"])
+    _same(n["uq"], uq, "u codes"), _same(n["us"], us, "u scales")
+    lin("uq", "us", "wd", "sd", "d", F)
+    h2, x2 = oracle.residual_norm(n["h1"], n["d"], n["g1"], None, 0, 1.0, n["g2"])
+    _same(n["h2"], h2, "h2"), _same(n["x2"], x2, "x2")
+
+
+def test_chain_captured_replayed_and_on_two_streams():
+    """Two chains in two graphs replayed at once on two streams, and run on a
+    side stream, give the bytes of their eager runs: no state is shared."""
+    m = vq()
+    sts = [_chain_state(m, M, 512, 1360, seed) for M, seed in ((4, 71), (200, 81))]
+    outs = ("h1", "xq", "xs", "u", "d", "h2", "x2")
+    want = []
+    for st in sts:
+        _block_chain(m, st)
+        want.append({k: st[k].clone() for k in outs})
+    torch.cuda.synchronize()
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st, stream in zip(sts, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            _block_chain(m, st)
+        graphs.append(g)
+    for st in sts:
+        for k in outs:
+            st[k].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for g, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    m.vlaq_check()
+    for st, w in zip(sts, want):
+        for k in outs:
+            assert torch.equal(st[k], w[k]), k
+            st[k].zero_()
+    torch.cuda.synchronize()
+    for st, stream in zip(sts, streams):
+        with torch.cuda.stream(stream):
+            _block_chain(m, st)
+    torch.cuda.synchronize()
+    for st, w in zip(sts, want):
+        for k in outs:
+            assert torch.equal(st[k], w[k]), k
+
+
+def test_weights_quantized_right_before_the_linear():
+    """The linear reads nothing before the kernels launched before it on the
+    stream: weights and activations quantized immediately before it."""
+    m = vq()
+    for M, N, K in ((1, 4608, 3584), (1024, 2560, 512)):
+        X, W = si.projection_activations(K, M, 3).cuda(), si.projection_weight(K, N, 3).cuda()
+        xq, sx = m.alloc_fp8_block(M, K)
+        wq, sw = m.alloc_fp8_block(N, K, weight=True)
+        Y, Y2 = (torch.empty(M, N, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        for order in range(2):
+            wq.fill_(0x7F), xq.fill_(0x7F)
+            torch.cuda.synchronize()
+            if order:
+                m.vlaq_quantize_weight_fp8_block(W, N, K, 0, wq, sw)
+                m.vlaq_quantize_act_fp8_block(X, M, K, None, 1e-6, 0, xq, sx)
+            else:
+                m.vlaq_quantize_act_fp8_block(X, M, K, None, 1e-6, 0, xq, sx)
+                m.vlaq_quantize_weight_fp8_block(W, N, K, 0, wq, sw)
+            m.vlaq_linear_fp8_block(xq, sx, wq, sw, None, Y2 if order else Y, M, N, K)
+        torch.cuda.synchronize()
+        assert torch.isfinite(Y.float()).all() and torch.equal(Y, Y2)

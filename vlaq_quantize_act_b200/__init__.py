@@ -25,7 +25,9 @@ __all__ = [
     "vlaq_selftest_wait_timeout",
     "vlaq_quantize_weight_fp8", "vlaq_quantize_act_fp8", "vlaq_linear_fp8", "vlaq_linear_nvfp4_noalloc",
     "vlaq_quantize_weight_int8", "vlaq_quantize_act_int8", "vlaq_linear_int8",
-    "alloc_nvfp4", "alloc_fp8", "alloc_int8", "alloc_workspace",
+    "vlaq_quantize_weight_fp8_block", "vlaq_quantize_act_fp8_block", "vlaq_linear_fp8_block",
+    "vlaq_residual_norm", "vlaq_residual_norm_fp8_block",
+    "alloc_nvfp4", "alloc_fp8", "alloc_fp8_block", "alloc_int8", "alloc_workspace",
 ]
 
 F_RMSNORM = 1
@@ -72,6 +74,12 @@ _SIGS = {
     "vlaq_selftest_wait_timeout": (ctypes.c_int, [_P]),
     "vlaq_quantize_act_nvfp4_smooth": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _F, _U32, _P, _P, _P, _P]),
     "vlaq_quantize_act_nvfp4_static": (ctypes.c_int, [_P, _I64, _I64, _P, _P, _F, _U32, _F, _P, _P, _P, _P]),
+    "vlaq_quantize_weight_fp8_block": (ctypes.c_int, [_P, _I64, _I64, _U32, _P, _P, _P]),
+    "vlaq_quantize_act_fp8_block": (ctypes.c_int, [_P, _I64, _I64, _P, _F, _U32, _P, _P, _P]),
+    "vlaq_linear_fp8_block": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P]),
+    "vlaq_residual_norm": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _F, _P, _P, _P]),
+    "vlaq_residual_norm_fp8_block": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _F, _U32, _P, _P, _P,
+                                                    _P]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -189,6 +197,34 @@ def vlaq_linear_fp8(xq, s_x, wq, s_w, residual, Y, M, N, K, workspace=None, ws_b
                                 _ptr(workspace), ws_bytes, _stream(stream)))
 
 
+# ------------------------------------------- FP8 with block scales of 128
+def vlaq_quantize_weight_fp8_block(W, N, K, flags, codes, s_w, stream=None):
+    _check(_lib.vlaq_quantize_weight_fp8_block(_ptr(W), N, K, flags, _ptr(codes), _ptr(s_w), _stream(stream)))
+
+
+def vlaq_quantize_act_fp8_block(X, M, K, gamma, eps, flags, codes, s_x, stream=None):
+    _check(_lib.vlaq_quantize_act_fp8_block(_ptr(X), M, K, _ptr(gamma), eps, flags, _ptr(codes), _ptr(s_x),
+                                            _stream(stream)))
+
+
+def vlaq_linear_fp8_block(xq, s_x, wq, s_w, residual, Y, M, N, K, stream=None):
+    _check(_lib.vlaq_linear_fp8_block(_ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w), _ptr(residual), _ptr(Y), M, N, K,
+                                      _stream(stream)))
+
+
+# --------------------------------------------------------- residual norm
+def vlaq_residual_norm(H, Y, M, K, gamma_post, gate, gate_rows, alpha, gamma_pre, eps, H_out, X_out, stream=None):
+    _check(_lib.vlaq_residual_norm(_ptr(H), _ptr(Y), M, K, _ptr(gamma_post), _ptr(gate), gate_rows, alpha,
+                                   _ptr(gamma_pre), eps, _ptr(H_out), _ptr(X_out), _stream(stream)))
+
+
+def vlaq_residual_norm_fp8_block(H, Y, M, K, gamma_post, gate, gate_rows, alpha, gamma_pre, eps, flags, H_out, codes,
+                                 s_x, stream=None):
+    _check(_lib.vlaq_residual_norm_fp8_block(_ptr(H), _ptr(Y), M, K, _ptr(gamma_post), _ptr(gate), gate_rows, alpha,
+                                             _ptr(gamma_pre), eps, flags, _ptr(H_out), _ptr(codes), _ptr(s_x),
+                                             _stream(stream)))
+
+
 # ------------------------------------------------------------------ INT8
 def vlaq_quantize_weight_int8(W, N, K, flags, codes, s_w, stream=None):
     _check(_lib.vlaq_quantize_weight_int8(_ptr(W), N, K, flags, _ptr(codes), _ptr(s_w), _stream(stream)))
@@ -218,6 +254,14 @@ def alloc_fp8(rows: int, K: int, device="cuda"):
     """(codes u8 [rows, K], scale f32 [rows])."""
     return (torch.empty(max(rows, 1), K, dtype=torch.uint8, device=device),
             torch.empty(max(rows, 1), dtype=torch.float32, device=device))
+
+
+def alloc_fp8_block(rows: int, K: int, device="cuda", weight: bool = False):
+    """(codes u8 [rows, K], block scales f32: [KB, rows] of activations, [NB, KB] of a weight)."""
+    kb = (K + 127) // 128
+    shape = ((rows + 127) // 128, kb) if weight else (kb, max(rows, 1))
+    return (torch.empty(max(rows, 1), K, dtype=torch.uint8, device=device),
+            torch.empty(shape, dtype=torch.float32, device=device))
 
 
 def alloc_int8(rows: int, K: int, device="cuda"):

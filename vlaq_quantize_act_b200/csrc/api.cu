@@ -97,6 +97,17 @@ vlaq_status check_flags(const char* fn, uint32_t flags, uint32_t allowed) {
   return VLAQ_OK;
 }
 
+vlaq_status check_linear_shape(const char* fn, bool fp4, int64_t M, int64_t N, int64_t K) {
+  vlaq_status st;
+  if ((st = check_k(fn, K, 0, fp4, 0))) return st;
+  if (M < 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = %lld is negative", fn, (long long)M);
+  if (N <= 0 || N % 8 != 0)
+    return fail(VLAQ_ERR_SHAPE, "%s: N = %lld must be a positive multiple of 8", fn, (long long)N);
+  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > 0x7FFFFFFF || M * N > (int64_t(1) << 40))
+    return fail(VLAQ_ERR_SHAPE, "%s: shape %lld x %lld x %lld too large", fn, (long long)M, (long long)N,
+                (long long)K);
+  return VLAQ_OK;
+}
 
 }  // namespace
 
@@ -121,6 +132,10 @@ vlaq_status vlaq_check(void* stream) {
   e = vlaq::read_and_clear_quant_status(&qst, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
   st |= qst;
+  unsigned int bst = 0;
+  e = vlaq::read_and_clear_block_status(&bst, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
+  st |= bst;
   if (st & vlaq::kStatusTimeout) {
     // a GEMM that gave up may have left split-K tile counters non-zero
     e = vlaq::noalloc_clear(static_cast<cudaStream_t>(stream));
@@ -335,13 +350,7 @@ static vlaq_status linear_common(const char* fn, LinearKind kind, const uint8_t*
                                  bool static_scratch = false) {
   vlaq_status st;
   const bool fp4 = kind == kLinearNvfp4;
-  if ((st = check_k(fn, K, 0, fp4, 0))) return st;
-  if (M < 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = %lld is negative", fn, (long long)M);
-  if (N <= 0 || N % 8 != 0)
-    return fail(VLAQ_ERR_SHAPE, "%s: N = %lld must be a positive multiple of 8", fn, (long long)N);
-  if (M > 0x7FFFFFFF || N > 0x7FFFFFFF || K > 0x7FFFFFFF || M * N > (int64_t(1) << 40))
-    return fail(VLAQ_ERR_SHAPE, "%s: shape %lld x %lld x %lld too large", fn, (long long)M, (long long)N,
-                (long long)K);
+  if ((st = check_linear_shape(fn, fp4, M, N, K))) return st;
   if (M == 0) return ok();
   VLAQ_NONNULL(fn, xq);
   VLAQ_NONNULL(fn, xg);
@@ -411,6 +420,148 @@ vlaq_status vlaq_linear_nvfp4_noalloc(const uint8_t* xq, const uint8_t* xs, cons
   // library's static scratch array (refused if it needs more)
   return linear_common("vlaq_linear_nvfp4_noalloc", kLinearNvfp4, xq, xs, g_x, wq, ws, g_w, residual, Y, M, N, K,
                        nullptr, 0, stream, true);
+}
+
+// ------------------------------------------------ FP8, block scales of 128
+vlaq_status vlaq_quantize_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
+                                           float* s_w, void* stream) {
+  const char* fn = "vlaq_quantize_weight_fp8_block";
+  vlaq_status st;
+  if ((st = check_flags(fn, flags, VLAQ_F_HADAMARD64))) return st;
+  if ((st = check_k(fn, K, flags, false, vlaq::kMaxQuantK))) return st;
+  if (N <= 0 || N > 0x7FFFFFFF) return fail(VLAQ_ERR_SHAPE, "%s: N = %lld out of range", fn, (long long)N);
+  VLAQ_NONNULL(fn, W);
+  VLAQ_NONNULL(fn, codes);
+  VLAQ_NONNULL(fn, s_w);
+  if ((st = check_device(fn))) return st;
+  cudaError_t e = vlaq::launch_quant_weight_fp8_block(W, N, K, flags, codes, s_w, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
+vlaq_status vlaq_quantize_act_fp8_block(const void* X, int64_t M, int64_t K, const void* gamma, float eps,
+                                        uint32_t flags, uint8_t* codes, float* s_x, void* stream) {
+  const char* fn = "vlaq_quantize_act_fp8_block";
+  vlaq_status st;
+  if ((st = check_flags(fn, flags, VLAQ_F_RMSNORM | VLAQ_F_HADAMARD64))) return st;
+  if ((st = check_k(fn, K, flags, false, vlaq::kMaxQuantK))) return st;
+  if (M < 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = %lld is negative", fn, (long long)M);
+  if (M > 0x7FFFFFFF) return fail(VLAQ_ERR_SHAPE, "%s: M = %lld is too large", fn, (long long)M);
+  if (M == 0) return ok();
+  VLAQ_NONNULL(fn, X);
+  VLAQ_NONNULL(fn, codes);
+  VLAQ_NONNULL(fn, s_x);
+  if (flags & VLAQ_F_RMSNORM) VLAQ_NONNULL(fn, gamma);
+  if ((st = check_device(fn))) return st;
+  cudaError_t e = vlaq::launch_quant_act_fp8_block(X, M, K, gamma, eps, flags, codes, s_x,
+                                                   static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
+vlaq_status vlaq_linear_fp8_block(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
+                                  const void* residual, void* Y, int64_t M, int64_t N, int64_t K, void* stream) {
+  const char* fn = "vlaq_linear_fp8_block";
+  vlaq_status st;
+  if ((st = check_linear_shape(fn, false, M, N, K))) return st;
+  if (M == 0) return ok();
+  VLAQ_NONNULL(fn, xq);
+  VLAQ_NONNULL(fn, s_x);
+  VLAQ_NONNULL(fn, wq);
+  VLAQ_NONNULL(fn, s_w);
+  VLAQ_NONNULL(fn, Y);
+  if (residual && !aligned16(residual)) return fail(VLAQ_ERR_ALIGN, "%s: residual is not 16-byte aligned", fn);
+  if ((st = check_device(fn))) return st;
+  vlaq::BlockLinear l = {};
+  l.xq = xq;
+  l.s_x = s_x;
+  l.wq = wq;
+  l.s_w = s_w;
+  l.residual = residual;
+  l.Y = Y;
+  l.M = M;
+  l.N = N;
+  l.K = K;
+  cudaError_t e = vlaq::launch_linear_fp8_block(l, vlaq::kWaitBudgetCycles, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
+static vlaq_status residual_norm_common(const char* fn, const vlaq::ResidualNorm& r, void* stream) {
+  vlaq_status st;
+  const void* H = r.H;
+  const void* Y = r.Y;
+  const void* H_out = r.H_out;
+  if ((st = check_k(fn, r.K, r.flags, false, vlaq::kMaxQuantK))) return st;
+  if (r.M < 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = %lld is negative", fn, (long long)r.M);
+  if (r.M > 0x7FFFFFFF) return fail(VLAQ_ERR_SHAPE, "%s: M = %lld is too large", fn, (long long)r.M);
+  if (!std::isfinite(r.alpha)) return fail(VLAQ_ERR_INVALID_ARG, "%s: alpha = %g is not finite", fn, (double)r.alpha);
+  if (r.gate && r.gate_rows <= 0)
+    return fail(VLAQ_ERR_INVALID_ARG, "%s: gate_rows = %lld must be positive with a gate", fn, (long long)r.gate_rows);
+  if (r.M == 0) return ok();
+  VLAQ_NONNULL(fn, H);
+  VLAQ_NONNULL(fn, Y);
+  VLAQ_NONNULL(fn, H_out);
+  if (!aligned16(r.gamma_post)) return fail(VLAQ_ERR_ALIGN, "%s: gamma_post is not 16-byte aligned", fn);
+  if (!aligned16(r.gate)) return fail(VLAQ_ERR_ALIGN, "%s: gate is not 16-byte aligned", fn);
+  if (r.codes || r.X_out) {
+    const void* gamma_pre = r.gamma_pre;
+    VLAQ_NONNULL(fn, gamma_pre);
+  }
+  if ((st = check_device(fn))) return st;
+  cudaError_t e = vlaq::launch_residual_norm(r, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
+vlaq_status vlaq_residual_norm(const void* H, const void* Y, int64_t M, int64_t K, const void* gamma_post,
+                               const void* gate, int64_t gate_rows, float alpha, const void* gamma_pre, float eps,
+                               void* H_out, void* X_out, void* stream) {
+  const char* fn = "vlaq_residual_norm";
+  vlaq::ResidualNorm r = {};
+  r.H = H;
+  r.Y = Y;
+  r.M = M;
+  r.K = K;
+  r.gamma_post = gamma_post;
+  r.gate = gate;
+  r.gate_rows = gate_rows;
+  r.alpha = alpha;
+  r.gamma_pre = gamma_pre;
+  r.eps = eps;
+  r.H_out = H_out;
+  r.X_out = X_out;
+  if (M != 0 && !aligned16(X_out)) return fail(VLAQ_ERR_ALIGN, "%s: X_out is not 16-byte aligned", fn);
+  return residual_norm_common(fn, r, stream);
+}
+
+vlaq_status vlaq_residual_norm_fp8_block(const void* H, const void* Y, int64_t M, int64_t K, const void* gamma_post,
+                                         const void* gate, int64_t gate_rows, float alpha, const void* gamma_pre,
+                                         float eps, uint32_t flags, void* H_out, uint8_t* codes, float* s_x,
+                                         void* stream) {
+  const char* fn = "vlaq_residual_norm_fp8_block";
+  vlaq_status st;
+  if ((st = check_flags(fn, flags, VLAQ_F_HADAMARD64))) return st;
+  vlaq::ResidualNorm r = {};
+  r.H = H;
+  r.Y = Y;
+  r.M = M;
+  r.K = K;
+  r.gamma_post = gamma_post;
+  r.gate = gate;
+  r.gate_rows = gate_rows;
+  r.alpha = alpha;
+  r.gamma_pre = gamma_pre;
+  r.eps = eps;
+  r.flags = flags;
+  r.H_out = H_out;
+  r.codes = codes;
+  r.s_x = s_x;
+  if (M > 0) {
+    VLAQ_NONNULL(fn, codes);
+    VLAQ_NONNULL(fn, s_x);
+  }
+  return residual_norm_common(fn, r, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,434 @@
+// FP8 quantizers with one scale per block of 128, and the residual update
+// between two blocks of a decoder (post norm, gate, residual scale, add, pre
+// norm) with a bf16 or FP8 block output.
+//
+//   s = max |v| / 448 over a block (1 x 128 of a token row, 128 x 128 of a
+//   weight), code = E4M3_rne_sat(v / s), 0 where s = 0; the arithmetic of the
+//   per-row FP8 quantizer in smaller scopes.
+//
+// Rows are split into 8-element chunks (16 bytes of bf16), chunk c on thread
+// c % T of a CTA of T threads, so 16 adjacent lanes hold one 1 x 128 block
+// and 8 adjacent lanes one 64-element Hadamard block; the block's amax is
+// four shuffles, and a warp reads 512 contiguous bytes per load.  All kernels
+// are bound by HBM for many rows (2 or 4 bytes in, 1 to 4 out per element)
+// and by the launch and one memory round trip for one row.
+//
+// Sums of squares use a fixed tree of 256 lanes, so a row's result does not
+// depend on how many rows the call has or on the CTA's thread count: lane l
+// owns the chunks l, l + 256, ... and adds them in element order with fused
+// multiply-adds; an XOR butterfly 16, 8, 4, 2, 1 joins each group of 32 lanes
+// and a butterfly 1, 2, 4 the eight groups.  A thread of a CTA with T < 256
+// threads carries 256 / T of these lanes.
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "quant_math.cuh"
+
+namespace vlaq {
+
+namespace {
+
+constexpr int kTreeLanes = 256;
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ float absmax8(const float* v) {
+  float m = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]));
+  return m;
+}
+
+// Normalised WHT of the 64-block on lanes 8 g .. 8 g + 7, 8 values each:
+// stages h = 1, 2, 4 in the lane, 8, 16, 32 across lanes (xor 1, 2, 4), then
+// x 1/8 (exact): the stages of the sequential butterfly in its order, each
+// sum or difference rounded once.  Executed by the whole warp.
+__device__ __forceinline__ void wht64_chunk(float* v, int lane) {
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & h) == 0) {
+        const float a = v[i], b = v[i + h];
+        v[i] = __fadd_rn(a, b);
+        v[i + h] = __fsub_rn(a, b);
+      }
+    }
+  }
+#pragma unroll
+  for (int x = 1; x < 8; x <<= 1) {
+    const float sg = (lane & x) != 0 ? -1.0f : 1.0f;  // upper lane: partner - own
+    const float2 s2 = make_float2(sg, sg);
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 p = make_float2(__shfl_xor_sync(0xffffffffu, v[i], x), __shfl_xor_sync(0xffffffffu, v[i + 1], x));
+      const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, p);
+      v[i] = r.x;
+      v[i + 1] = r.y;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], 0.125f);
+}
+
+// Codes of 8 values of a block with divisor d: two words, element 0 lowest.
+__device__ __forceinline__ uint2 e4m3_codes8(const float* v, const Divisor& d) {
+  float q[8];
+  quotients<8>(v, d, q);
+  return make_uint2(cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16),
+                    cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16));
+}
+
+// Scale of the 1 x 128 block on 16 adjacent lanes.  Executed by the warp.
+__device__ __forceinline__ float block_scale16(const float* v) {
+  float m = absmax8(v);
+#pragma unroll
+  for (int x = 1; x < 16; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  return row_global<1>(m);
+}
+
+// ------------------------------------------------------ activation blocks --
+// Without a norm the blocks of all rows are independent: 16 lanes take one
+// block, kUnroll blocks each with their loads in flight together.
+struct BlocksArgs {
+  const __nv_bfloat16* X;
+  int64_t rows, K;
+  int64_t blocks;                  // per row
+  int64_t total;                   // rows * blocks
+  unsigned long long inv_blocks;   // floor(2^64 / blocks) + 1 (blocks > 1)
+  uint8_t* codes;
+  float* scales;                   // [blocks][rows]
+};
+
+constexpr int kBlocksThreads = 256;
+constexpr int kUnroll = 4;
+constexpr int kGroups = kBlocksThreads / 16;
+
+template <bool WHT>
+__global__ void __launch_bounds__(kBlocksThreads) quant_blocks_kernel(const BlocksArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int group = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kUnroll * kGroups) + group;
+  uint4 d[kUnroll];
+  int64_t off[kUnroll];  // element offset of this lane's chunk, -1 past the data
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    const int64_t i = first + u * kGroups;
+    // i / blocks: exact while i * blocks < 2^64
+    const int64_t row = a.blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
+    const int64_t k = (i - row * a.blocks) * 128 + 8 * sub;
+    off[u] = i < a.total && k < a.K ? row * a.K + k : -1;
+    d[u] = off[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.X + off[u])) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    float v[8];
+    unpack_bf16x8(d[u], v);
+    if (WHT) wht64_chunk(v, threadIdx.x & 31);
+    const float s = block_scale16(v);
+    const uint2 w = e4m3_codes8(v, make_divisor(s));
+    if (off[u] >= 0) {
+      *reinterpret_cast<uint2*>(a.codes + off[u]) = w;
+      if (sub == 0) {
+        const int64_t i = first + u * kGroups;
+        const int64_t row = a.blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
+        a.scales[(i - row * a.blocks) * a.rows + row] = s;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------ weight blocks --
+// One CTA per 128 x 128 block: 16 lanes cover a row's 128 columns, 16 rows at
+// a time; the whole block stays in registers (8 chunks per thread) between
+// the amax and the codes, so W is read once.
+constexpr int kWeightThreads = 256;
+
+template <bool WHT>
+__global__ void __launch_bounds__(kWeightThreads) quant_weight_block_kernel(const __nv_bfloat16* W, int64_t N,
+                                                                             int64_t K, uint8_t* codes,
+                                                                             float* scales) {
+  __shared__ float s_max[kWeightThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4, lane = threadIdx.x & 31;
+  const int64_t k_blocks = (K + 127) / 128;
+  const int64_t nb = blockIdx.x / k_blocks, kb = blockIdx.x % k_blocks;
+  const int64_t k = kb * 128 + 8 * sub;
+  uint4 d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t n = nb * 128 + r0 + 16 * i;
+    d[i] = n < N && k < K ? __ldg(reinterpret_cast<const uint4*>(W + n * K + k)) : make_uint4(0, 0, 0, 0);
+  }
+  float v[WHT ? 8 : 1][8];
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t[8];
+    unpack_bf16x8(d[i], t);
+    if (WHT) {
+      wht64_chunk(t, lane);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = t[j];
+    }
+    m = fmaxf(m, absmax8(t));
+  }
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // m >= 0: bit order is value order
+  if (lane == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWeightThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+  const float s = row_global<1>(m);
+  const Divisor dv = make_divisor(s);
+  if (threadIdx.x == 0) scales[blockIdx.x] = s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float t[8];
+    if (WHT) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = v[i][j];
+    } else {
+      unpack_bf16x8(d[i], t);
+    }
+    const uint2 w = e4m3_codes8(t, dv);
+    const int64_t n = nb * 128 + r0 + 16 * i;
+    if (n < N && k < K) *reinterpret_cast<uint2*>(codes + n * K + k) = w;
+  }
+}
+
+// --------------------------------------------------- rows with a norm --
+// One CTA per row, the row in registers (CPT chunks of 8 per thread).
+//   RESID:  t = RMSNorm(y) (or y), t *= gate, c = h + alpha t, h' = bf16(c)
+//   else:   c = x
+//   then    v = RMSNorm(c) from the unrounded fp32 c (skipped when the call
+//           asks for no x), and v as bf16, or rotated and as FP8 blocks.
+enum { kOutBf16 = 0, kOutFp8 = 1 };
+
+struct NormArgs {
+  const __nv_bfloat16* h;  // residual stream, or x without RESID
+  const __nv_bfloat16* y;
+  const __nv_bfloat16* gamma_post;  // may be null: no post norm
+  const __nv_bfloat16* gate;        // may be null: 1
+  int64_t gate_rows;
+  float alpha;
+  const __nv_bfloat16* gamma_pre;
+  float eps;
+  __nv_bfloat16* h_out;
+  __nv_bfloat16* x_out;  // kOutBf16; null: no x
+  uint8_t* codes;        // kOutFp8
+  float* scales;         // [blocks][rows]
+  int64_t rows;
+  int K;
+};
+
+// Sum of squares of a row in the 256-lane tree.  v: the thread's chunks in
+// order (chunk i is chunk t + T i of the row, zeros past it).
+template <int T, int CPT>
+__device__ __forceinline__ float tree_sumsq(const float (&v)[CPT][8], float* s_part) {
+  constexpr int L = kTreeLanes / T;  // tree lanes per thread
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int l = 0; l < L; ++l) {
+    float acc = 0.0f;
+#pragma unroll
+    for (int i = l; i < CPT; i += L)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc = __fmaf_rn(v[i][j], v[i][j], acc);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
+    if (lane == 0) s_part[warp + (T / 32) * l] = acc;  // group of tree lanes 32 g .. 32 g + 31
+  }
+  __syncthreads();
+  const float* p = s_part;
+  return __fadd_rn(__fadd_rn(__fadd_rn(p[0], p[1]), __fadd_rn(p[2], p[3])),
+                   __fadd_rn(__fadd_rn(p[4], p[5]), __fadd_rn(p[6], p[7])));
+}
+
+__device__ __forceinline__ float rms_factor(float ss, int K, float eps) {
+  const float mean = __fdiv_rn(ss, static_cast<float>(K));
+  return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
+}
+
+// v = (v r) gamma for the thread's chunks.
+template <int T, int CPT>
+__device__ __forceinline__ void apply_norm(float (&v)[CPT][8], float r, const __nv_bfloat16* gamma, int chunks) {
+#pragma unroll
+  for (int i = 0; i < CPT; ++i) {
+    const int c = threadIdx.x + T * i;
+    if (c < chunks) {
+      float g[8];
+      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(gamma) + c), g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(__fmul_rn(v[i][j], r), g[j]);
+    }
+  }
+}
+
+template <bool RESID, bool WHT, int OUT, int T, int CPT>
+__global__ void __launch_bounds__(T) norm_rows_kernel(const NormArgs a) {
+  __shared__ float s_part[2][kTreeLanes / 32];
+  const int K = a.K, chunks = K >> 3;
+  const int lane = threadIdx.x & 31;
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    // plain loads of h and y: the outputs may overwrite them in place
+    const uint4* h4 = reinterpret_cast<const uint4*>(a.h + row * K);
+    uint4 hw[CPT];
+    float v[CPT][8];
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = threadIdx.x + T * i;
+      hw[i] = c < chunks ? h4[c] : make_uint4(0, 0, 0, 0);
+    }
+    if (RESID) {
+      const uint4* y4 = reinterpret_cast<const uint4*>(a.y + row * K);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + T * i;
+        unpack_bf16x8(c < chunks ? y4[c] : make_uint4(0, 0, 0, 0), v[i]);
+      }
+      if (a.gamma_post) {
+        const float ss = tree_sumsq<T, CPT>(v, s_part[0]);
+        apply_norm<T, CPT>(v, rms_factor(ss, K, a.eps), a.gamma_post, chunks);
+      }
+      if (a.gate) {
+        const uint4* g4 = reinterpret_cast<const uint4*>(a.gate + (row / a.gate_rows) * K);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) {
+          const int c = threadIdx.x + T * i;
+          if (c < chunks) {
+            float g[8];
+            unpack_bf16x8(__ldg(g4 + c), g);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], g[j]);
+          }
+        }
+      }
+      uint4* o4 = reinterpret_cast<uint4*>(a.h_out + row * K);
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) {
+        const int c = threadIdx.x + T * i;
+        float h[8];
+        unpack_bf16x8(hw[i], h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = __fadd_rn(h[j], __fmul_rn(v[i][j], a.alpha));
+        if (c < chunks) o4[c] = pack_bf16x8(v[i]);
+      }
+      if (OUT == kOutBf16 && !a.x_out) {
+        __syncthreads();  // the next row reuses s_part
+        continue;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < CPT; ++i) unpack_bf16x8(hw[i], v[i]);
+    }
+    const float ss = tree_sumsq<T, CPT>(v, s_part[1]);
+    apply_norm<T, CPT>(v, rms_factor(ss, K, a.eps), a.gamma_pre, chunks);
+#pragma unroll
+    for (int i = 0; i < CPT; ++i) {
+      const int c = threadIdx.x + T * i;
+      if (OUT == kOutBf16) {
+        if (c < chunks) reinterpret_cast<uint4*>(a.x_out + row * K)[c] = pack_bf16x8(v[i]);
+      } else if ((c & ~31) < chunks) {  // warp-uniform
+        if (WHT) wht64_chunk(v[i], lane);
+        const float s = block_scale16(v[i]);
+        const uint2 w = e4m3_codes8(v[i], make_divisor(s));
+        if (c < chunks) {
+          *reinterpret_cast<uint2*>(a.codes + row * K + 8 * c) = w;
+          if ((c & 15) == 0) a.scales[static_cast<int64_t>(c >> 4) * a.rows + row] = s;
+        }
+      }
+    }
+    __syncthreads();  // the next row reuses s_part
+  }
+}
+
+template <bool RESID, bool WHT, int OUT, int T, int CPT>
+cudaError_t launch_norm_shape(const NormArgs& a, cudaStream_t s) {
+  // one row per CTA; very tall inputs loop (at most 64 CTAs per SM are launched)
+  const int64_t cap = static_cast<int64_t>(device_sm_count()) * 64;
+  const unsigned int grid = static_cast<unsigned int>(a.rows < cap ? a.rows : cap);
+  return launch_pdl(norm_rows_kernel<RESID, WHT, OUT, T, CPT>, dim3(grid), dim3(T), 0, s, a);
+}
+
+template <bool RESID, bool WHT, int OUT>
+cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
+  if (a.K <= 2048) return launch_norm_shape<RESID, WHT, OUT, 256, 1>(a, s);
+  if (a.K <= 4096) return launch_norm_shape<RESID, WHT, OUT, 256, 2>(a, s);
+  if (a.K <= 8192) return launch_norm_shape<RESID, WHT, OUT, 256, 4>(a, s);
+  return launch_norm_shape<RESID, WHT, OUT, 256, 16>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, const void* gamma, float eps,
+                                       uint32_t flags, uint8_t* codes, float* s_x, cudaStream_t s) {
+  const bool wht = (flags & kFlagHadamard) != 0;
+  if (flags & kFlagRmsNorm) {
+    NormArgs a = {};
+    a.h = static_cast<const __nv_bfloat16*>(X);
+    a.gamma_pre = static_cast<const __nv_bfloat16*>(gamma);
+    a.eps = eps;
+    a.codes = codes;
+    a.scales = s_x;
+    a.rows = M;
+    a.K = static_cast<int>(K);
+    return wht ? launch_norm<false, true, kOutFp8>(a, s) : launch_norm<false, false, kOutFp8>(a, s);
+  }
+  BlocksArgs a;
+  a.X = static_cast<const __nv_bfloat16*>(X);
+  a.rows = M;
+  a.K = K;
+  a.blocks = (K + 127) / 128;
+  a.total = M * a.blocks;
+  a.inv_blocks = a.blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(a.blocks) + 1;
+  a.codes = codes;
+  a.scales = s_x;
+  const int64_t grid = (a.total + kUnroll * kGroups - 1) / (kUnroll * kGroups);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(wht ? quant_blocks_kernel<true> : quant_blocks_kernel<false>,
+                    dim3(static_cast<unsigned int>(grid)), dim3(kBlocksThreads), 0, s, a);
+}
+
+cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
+                                          float* s_w, cudaStream_t s) {
+  const int64_t grid = ((N + 127) / 128) * ((K + 127) / 128);
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl((flags & kFlagHadamard) ? quant_weight_block_kernel<true> : quant_weight_block_kernel<false>,
+                    dim3(static_cast<unsigned int>(grid)), dim3(kWeightThreads), 0, s,
+                    static_cast<const __nv_bfloat16*>(W), N, K, codes, s_w);
+}
+
+cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s) {
+  NormArgs a = {};
+  a.h = static_cast<const __nv_bfloat16*>(r.H);
+  a.y = static_cast<const __nv_bfloat16*>(r.Y);
+  a.gamma_post = static_cast<const __nv_bfloat16*>(r.gamma_post);
+  a.gate = static_cast<const __nv_bfloat16*>(r.gate);
+  a.gate_rows = r.gate_rows;
+  a.alpha = r.alpha;
+  a.gamma_pre = static_cast<const __nv_bfloat16*>(r.gamma_pre);
+  a.eps = r.eps;
+  a.h_out = static_cast<__nv_bfloat16*>(r.H_out);
+  a.x_out = static_cast<__nv_bfloat16*>(r.X_out);
+  a.codes = r.codes;
+  a.scales = r.s_x;
+  a.rows = r.M;
+  a.K = static_cast<int>(r.K);
+  if (!r.codes) return launch_norm<true, false, kOutBf16>(a, s);
+  return (r.flags & kFlagHadamard) ? launch_norm<true, true, kOutFp8>(a, s) : launch_norm<true, false, kOutFp8>(a, s);
+}
+
+}  // namespace vlaq

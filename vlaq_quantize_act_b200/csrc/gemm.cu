@@ -39,6 +39,7 @@
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace vlaq {
 
@@ -1451,8 +1452,6 @@ EncodeTiledFn get_encode_fn() {
   return fn;
 }
 
-// 2-D byte tensor [rows, row_bytes] with the given pitch, box 128 x box_rows,
-// 128-byte swizzle, zero fill out of bounds.
 // 8-bit GEMM over CTA pairs (prefill shapes): FP8 E4M3 (kind::f8f6f4, fp32
 // accumulators) or INT8 (I8: kind::i8, exact s32), 256 x 256 tiles of the
 // paired MMA (tcgen05.mma.cta_group::2) across the two CTAs of a cluster.
@@ -1716,6 +1715,8 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   }
 }
 
+}  // namespace
+
 bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
               uint32_t box_rows) {
   EncodeTiledFn enc = get_encode_fn();
@@ -1728,6 +1729,8 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t r
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // bf16 output [rows, cols] for TMA tile stores: box 64 columns x 32 rows
 // (128-byte rows), 128-byte swizzle.  Needs a 16-byte aligned base and

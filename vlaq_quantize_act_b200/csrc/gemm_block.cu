@@ -1,0 +1,768 @@
+// FP8 E4M3 GEMM with block scales of 128 on the sm_100a tensor cores.
+//
+//   Y[m, n] = bf16_rne( sum_b s_x[b, m] s_w[n / 128, b] P_b[m, n] + residual[m, n] )
+//   P_b[m, n] = sum_{k in block b} e4m3(x[m, k]) e4m3(w[n, k])
+//
+// The fp32 scales cannot go into the MMA (its block scales are powers of two
+// or E4M3), so each block of 128 along K is one accumulation of its own in
+// TMEM (four MMAs of K = 32), and epilogue warps add it, scaled, to fp32 sums
+// that stay in their registers: acc = fma(P_b, s_x s_w, acc).  One
+// accumulator buffer is read while the next block's MMAs fill another.
+//   gemm_block_pair_kernel  256 x 256 tiles over the two CTAs of a cluster
+//                           (paired MMA), token rows on the TMEM lanes: one
+//                           scale per thread and block; prefill shapes.
+//   gemm_block_cols_kernel  128 weight rows on the TMEM lanes and NT token
+//                           columns (16 .. 128): a decode step's tile is as
+//                           narrow as its tokens, and the tile reads each
+//                           weight once; K is split over the CTAs of a cluster,
+//                           whose sums meet in shared memory (no workspace,
+//                           fixed order); decode and small shapes.
+//
+// Every mbarrier wait is bounded (clock budget); a wait that runs out sets a
+// shared abort flag and the device status word, the roles drain their own
+// in-flight copies and MMAs, TMEM is freed and the kernel returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+
+#include "internal.h"
+#include "ptx.cuh"
+#include "tensor_map.h"
+
+namespace vlaq {
+
+__device__ unsigned int g_vlaq_block_status = 0;
+
+namespace {
+
+constexpr int kTmemColumns = 512;
+constexpr int kRowBytes = 128;              // one block of 128 codes of a row
+constexpr int kTileBytes = 128 * kRowBytes;  // 128 rows of it
+
+struct BlockArgs {
+  const float* sx;  // [blocks][M]
+  const float* sw;  // [ceil(N / 128)][blocks]
+  const __nv_bfloat16* residual;
+  __nv_bfloat16* Y;
+  int M, N;
+  int blocks;       // ceil(K / 128)
+  int m_tiles, n_tiles, units;
+  long long budget;
+};
+
+__device__ __forceinline__ void give_up(volatile int* abort_flag) {
+  *abort_flag = 1;
+  atomicOr(&g_vlaq_block_status, kStatusTimeout);
+}
+
+// Bounded wait that also gives up once another role (or, in a pair, a role of
+// the other CTA: peer_abort != 0) aborted.
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, long long budget,
+                                             volatile int* abort_flag, uint32_t peer_abort) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > budget) {
+      give_up(abort_flag);
+      if (peer_abort) st_shared_cluster_u32(peer_abort, 1u);
+      return false;
+    }
+  }
+}
+
+// The same by all lanes of a warp, which leave together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long budget, volatile int* abort_flag,
+                                          uint32_t peer_abort) {
+  return __all_sync(0xffffffffu, bounded_wait(bar, parity, budget, abort_flag, peer_abort));
+}
+
+// acc[j] += p[j] s for 32 columns, two per instruction.
+__device__ __forceinline__ void add_scaled32(float2* acc, const uint32_t (&p)[32], float s) {
+  const float2 ss = make_float2(s, s);
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    acc[j] = __ffma2_rn(make_float2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1])), ss, acc[j]);
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ---------------------------------------------------------------------------
+// CTA r of a pair loads rows [128 r, 128 r + 128) of the x tile and of the w
+// tile; the paired MMA gives it the 128 x 256 accumulator of its own rows.
+// Two 256-column accumulator buffers fill TMEM; block i uses buffer i % 2.
+// One barrier pair per stage carries everything the MMA thread waits for: the
+// leader's full barrier of block i completes on both CTAs' operand bytes and
+// on the 16 epilogue warps that have read block i - 2 out of its buffer, and
+// one commit per block to both CTAs' done barrier tells the producers that the
+// stage is free and the epilogue warps that the block's sums are there.
+//   warp 0: producer; warp 1: TMEM allocator (both) and MMA issuer (leader);
+//   warps 2, 3: idle; warps 4-11: epilogue, warp e = w - 4 has TMEM lanes
+//   32 (w % 4) .. + 31 (its token rows) and columns 128 (e / 4) .. + 127 (one
+//   weight scale per block).
+// The sums take 128 registers per epilogue thread: warps 0-3 give theirs up
+// (40), warps 4-11 take 232: 40 + 2 * 232 = 3 * 168 (the build checks that
+// ptxas allocates 168 at entry).
+struct PairTile {
+  static constexpr int BM = 256, BN = 256;
+  static constexpr int STAGE_BYTES = 2 * kTileBytes;
+  static constexpr int STAGES = 6;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = 256, M = 256
+  static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTile::THREADS, 1)
+gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const BlockArgs a) {
+  using C = PairTile;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];  // leader: operands of both CTAs, buffer read
+  __shared__ __align__(8) uint64_t done_bar[C::STAGES];  // block accumulated (leader's commit)
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const int pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full_bar[i], 1 + 2 * C::EPI_WARPS);
+      mbar_init(&done_bar[i], 1);
+    }
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(&s_tmem_base, kTmemColumns);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // both CTAs' barriers are initialised before either CTA signals the other's
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base;
+  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&s_abort)), rank ^ 1u);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp < 4) {
+    regs_dec<40>();
+    if (warp == 0 && lane == 0) {
+      // ----------------------------------------------------------- producer
+      int it = 0;
+      bool ok = true;
+      uint32_t armed_phase = 0;  // per stage: parity of the last armed phase
+      for (int u = pair; u < a.units && ok; u += pairs) {
+        const int m0 = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank);
+        const int n0 = (u / a.m_tiles) * C::BN + 128 * static_cast<int>(rank);
+        for (int b = 0; b < a.blocks; ++b, ++it) {
+          const int stage = it % C::STAGES;
+          const uint32_t phase = static_cast<uint32_t>(it / C::STAGES) & 1u;
+          if (it >= C::STAGES && !bounded_wait(&done_bar[stage], phase ^ 1u, a.budget, &s_abort, peer_abort)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE_BYTES);
+          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+          uint8_t* sx = smem + stage * C::STAGE_BYTES;
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0u);
+          tma_load_2d_pair(sx, &tmX, bar, b * kRowBytes, m0);
+          tma_load_2d_pair(sx + kTileBytes, &tmW, bar, b * kRowBytes, n0);
+        }
+      }
+      if (ok) {
+        // the leader's last commits have landed in this CTA
+        for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+          bounded_wait(&done_bar[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, a.budget, &s_abort,
+                       peer_abort);
+      } else if (rank == 0) {
+        // let every load in flight land before the pair's final barrier
+        for (int i = 0; i < C::STAGES && i < it; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&full_bar[i], (armed_phase >> i) & 1u) && clock64() - t0 < (1ll << 21)) {
+          }
+        }
+      } else {
+        // the peer cannot observe the leader's barriers: time instead
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 21)) {
+        }
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ------------------------------------------------- MMA issuer (leader)
+      int it = 0;
+      bool ok = true;
+      for (int u = pair; u < a.units && ok; u += pairs) {
+        for (int b = 0; b < a.blocks; ++b, ++it) {
+          const int stage = it % C::STAGES;
+          if (!bounded_wait(&full_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort,
+                            peer_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES), b0 = a0 + kTileBytes;
+          const uint32_t d = tmem + static_cast<uint32_t>((it & 1) * C::BN);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f8f6f4_pair(d, sdesc_kmajor_sw128(a0 + 32 * j), sdesc_kmajor_sw128(b0 + 32 * j), C::IDESC, j > 0);
+          umma_commit_pair(&done_bar[stage], 0x3);
+        }
+      }
+      umma_commit_pair(&drain_bar, 0x1);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
+      }
+    }
+  } else {
+    // ------------------------------------------------- epilogue (both CTAs)
+    regs_inc<232>();
+    const int q = warp & 3;
+    const int h = (warp - 4) >> 2;
+    auto buffer_read = [&](int block) {  // this warp is done with the buffer that block reuses
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[block % C::STAGES]), 0u));
+    };
+    buffer_read(0);
+    buffer_read(1);
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(128 * h);
+    int it = 0;
+    bool ok = true;
+    for (int u = pair; u < a.units && ok; u += pairs) {
+      const int row = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank) + 32 * q + lane;
+      const int col0 = (u / a.m_tiles) * C::BN + 128 * h;
+      const bool live = row < a.M && col0 < a.N;
+      // scales of four blocks at a time, the next four in flight meanwhile
+      const float* sxp = a.sx + row;
+      const float* swp = a.sw + static_cast<int64_t>(col0 >> 7) * a.blocks;
+      auto scale = [&](int b) {
+        return live && b < a.blocks ? __ldg(sxp + static_cast<int64_t>(b) * a.M) * __ldg(swp + b) : 0.0f;
+      };
+      float2 acc[64];
+#pragma unroll
+      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
+      float next[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) next[t] = scale(t);
+      for (int b0 = 0; b0 < a.blocks && ok; b0 += 4) {
+        float cur[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          cur[t] = next[t];
+          next[t] = scale(b0 + 4 + t);
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (b0 + t >= a.blocks) break;
+          const int stage = it % C::STAGES;
+          if (!warp_wait(&done_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort,
+                         peer_abort)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tb = tbase + static_cast<uint32_t>((it & 1) * C::BN);
+          uint32_t p0[32], p1[32];
+          tmem_ld_32x32b_x32(tb, p0);
+          tmem_ld_wait();
+          tmem_ld_32x32b_x32(tb + 32, p1);
+          add_scaled32(acc, p0, cur[t]);
+          tmem_ld_wait();
+          tmem_ld_32x32b_x32(tb + 64, p0);
+          add_scaled32(acc + 16, p1, cur[t]);
+          tmem_ld_wait();
+          tmem_ld_32x32b_x32(tb + 96, p1);
+          add_scaled32(acc + 32, p0, cur[t]);
+          tmem_ld_wait();
+          buffer_read(it + 2);
+          add_scaled32(acc + 48, p1, cur[t]);
+          ++it;
+        }
+      }
+      if (!ok) break;
+      if (live) {
+        const size_t base = static_cast<size_t>(row) * a.N + col0;
+        __nv_bfloat16* yp = a.Y + base;
+        const __nv_bfloat16* rp = a.residual ? a.residual + base : nullptr;
+#pragma unroll
+        for (int g = 0; g < 16; ++g) {  // 8 columns each; N % 8 == 0: in or out as a whole
+          if (col0 + 8 * g < a.N) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              y[2 * j] = acc[4 * g + j].x;
+              y[2 * j + 1] = acc[4 * g + j].y;
+            }
+            if (rp) {
+              const uint4 rv = *reinterpret_cast<const uint4*>(rp + 8 * g);
+              const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                y[2 * j] += __uint_as_float(rw[j] << 16);
+                y[2 * j + 1] += __uint_as_float(rw[j] & 0xFFFF0000u);
+              }
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = bf16x2(y[2 * j], y[2 * j + 1]);
+            *reinterpret_cast<uint4*>(yp + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+    }
+  }
+
+  // Neither CTA leaves (or frees its TMEM) while the other may still signal
+  // it or the paired MMAs may still touch its shared memory or TMEM.
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, kTmemColumns);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tile: 128 weight rows (MMA rows, TMEM lanes) x NT tokens (columns).  The
+// CTAs of a cluster share a tile and take consecutive ranges of its blocks; a
+// cluster of one loops over tiles.
+//   warp 0: producer; warp 1: TMEM allocator and MMA issuer; warp 2: scales
+//   (the products s_x s_w of a block, one per column, in shared memory);
+//   warp 3: idle; warps 4 ..: epilogue, warp e = w - 4 has weight rows 32 (w %
+//   4) .. + 31 and columns COLS (e / 4) .. + COLS - 1.
+template <int NT>
+struct ColsTile {
+  static constexpr int BN = 128;  // weight rows
+  static constexpr int X_BYTES = NT * kRowBytes;
+  static constexpr int STAGE_BYTES = kTileBytes + X_BYTES;
+  static constexpr int STAGES = (196 * 1024) / STAGE_BYTES > 10 ? 10 : (196 * 1024) / STAGE_BYTES;
+  static constexpr int BUFS = 4;  // accumulator buffers (and scale slots)
+  static constexpr int EPI_WARPS = NT >= 64 ? 8 : 4;
+  static constexpr int COLS = NT / (EPI_WARPS / 4);
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int TMEM_COLS = BUFS * NT;  // a power of two, >= 32
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = NT, M = 128
+  static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(BN >> 4) << 24);
+  static_assert(NT * BN * 4 <= STAGES * STAGE_BYTES, "the cluster's sums fit the operand ring");
+  static_assert(TMEM_COLS <= kTmemColumns, "TMEM budget");
+};
+
+template <int COLS>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[COLS]);
+template <>
+__device__ __forceinline__ void tmem_ld_cols<32>(uint32_t taddr, uint32_t (&r)[32]) {
+  tmem_ld_32x32b_x32(taddr, r);
+}
+template <>
+__device__ __forceinline__ void tmem_ld_cols<16>(uint32_t taddr, uint32_t (&r)[16]) {
+  tmem_ld_32x32b_x16(taddr, r);
+}
+
+template <int NT>
+__global__ void __launch_bounds__(ColsTile<NT>::THREADS, 1)
+gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const BlockArgs a, const int splits) {
+  using C = ColsTile<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];   // operands of a block
+  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];  // block consumed
+  __shared__ __align__(8) uint64_t accf_bar[C::BUFS];     // block accumulated
+  __shared__ __align__(8) uint64_t scf_bar[C::BUFS];      // block's scales written
+  __shared__ __align__(8) uint64_t acce_bar[C::BUFS];     // accumulator and scales read
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(16) float s_scale[C::BUFS][NT];
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = static_cast<int>(blockIdx.x) / splits;
+  const int groups = static_cast<int>(gridDim.x) / splits;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / splits);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / splits);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full_bar[i], 1);
+      mbar_init(&empty_bar[i], 1);
+    }
+    for (int i = 0; i < C::BUFS; ++i) {
+      mbar_init(&accf_bar[i], 1);
+      mbar_init(&scf_bar[i], 1);
+      mbar_init(&acce_bar[i], C::EPI_WARPS);
+    }
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmW);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- producer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      uint32_t armed_phase = 0;
+      for (int u = group; u < a.units && ok; u += groups) {
+        const int m0 = (u % a.m_tiles) * NT, n0 = (u / a.m_tiles) * C::BN;
+        for (int b = kb0; b < kb1; ++b, ++it) {
+          const int stage = it % C::STAGES;
+          const uint32_t phase = static_cast<uint32_t>(it / C::STAGES) & 1u;
+          if (!bounded_wait(&empty_bar[stage], phase ^ 1u, a.budget, &s_abort, 0)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
+          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
+          uint8_t* sw = smem + stage * C::STAGE_BYTES;
+          tma_load_2d(sw, &tmW, &full_bar[stage], b * kRowBytes, n0);
+          tma_load_2d(sw + kTileBytes, &tmX, &full_bar[stage], b * kRowBytes, m0);
+        }
+      }
+      if (!ok) {
+        // let every load in flight land before teardown
+        for (int i = 0; i < C::STAGES && i < it; ++i) {
+          const long long t0 = clock64();
+          while (!mbar_try_wait(&full_bar[i], (armed_phase >> i) & 1u) && clock64() - t0 < a.budget) {
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ----------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int u = group; u < a.units && ok; u += groups) {
+        for (int b = kb0; b < kb1; ++b, ++it) {
+          const int stage = it % C::STAGES, buf = it % C::BUFS;
+          if (!bounded_wait(&acce_bar[buf], (static_cast<uint32_t>(it / C::BUFS) & 1u) ^ 1u, a.budget, &s_abort, 0) ||
+              !bounded_wait(&full_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort, 0)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t w0 = smem_u32(smem + stage * C::STAGE_BYTES), x0 = w0 + kTileBytes;
+          const uint32_t d = tmem + static_cast<uint32_t>(buf * NT);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            mma_f8f6f4(d, sdesc_kmajor_sw128(w0 + 32 * j), sdesc_kmajor_sw128(x0 + 32 * j), C::IDESC, j > 0);
+          umma_commit(&empty_bar[stage]);
+          umma_commit(&accf_bar[buf]);
+        }
+      }
+      umma_commit(&drain_bar);
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
+      }
+    }
+  } else if (warp == 2) {
+    // --------------------------------------------------------------- scales
+    constexpr int PER_LANE = (NT + 31) / 32;
+    int it = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      const int m0 = (u % a.m_tiles) * NT, nb = u / a.m_tiles;
+      const float* swp = a.sw + static_cast<int64_t>(nb) * a.blocks;
+      constexpr int AHEAD = 4;  // blocks loaded ahead of use
+      float next[AHEAD][PER_LANE];
+      auto load = [&](int b, float (&s)[PER_LANE]) {
+        const float w = b < kb1 ? __ldg(swp + b) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i) {
+          const int m = m0 + lane + 32 * i;
+          s[i] = b < kb1 && lane + 32 * i < NT && m < a.M ? w * __ldg(a.sx + static_cast<int64_t>(b) * a.M + m) : 0.0f;
+        }
+      };
+#pragma unroll
+      for (int t = 0; t < AHEAD; ++t) load(kb0 + t, next[t]);
+      for (int b0 = kb0; b0 < kb1 && ok; b0 += AHEAD) {
+#pragma unroll
+        for (int t = 0; t < AHEAD; ++t) {
+          if (b0 + t >= kb1) break;
+          const int buf = it % C::BUFS;
+          if (!warp_wait(&acce_bar[buf], (static_cast<uint32_t>(it / C::BUFS) & 1u) ^ 1u, a.budget, &s_abort, 0)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < PER_LANE; ++i)
+            if (lane + 32 * i < NT) s_scale[buf][lane + 32 * i] = next[t][i];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&scf_bar[buf]);
+          load(b0 + AHEAD + t, next[t]);
+          ++it;
+        }
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- epilogue
+    constexpr int CH = C::COLS < 32 ? C::COLS : 32;  // columns per TMEM load
+    const int q = warp & 3;
+    const int col0 = ((warp - 4) >> 2) * C::COLS;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(col0);
+    int it = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      const int m0 = (u % a.m_tiles) * NT, n0 = (u / a.m_tiles) * C::BN;
+      float acc[C::COLS];
+#pragma unroll
+      for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+      for (int b = kb0; b < kb1; ++b, ++it) {
+        const int buf = it % C::BUFS;
+        const uint32_t phase = static_cast<uint32_t>(it / C::BUFS) & 1u;
+        if (!warp_wait(&scf_bar[buf], phase, a.budget, &s_abort, 0) ||
+            !warp_wait(&accf_bar[buf], phase, a.budget, &s_abort, 0)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const float* sc = &s_scale[buf][col0];
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += CH) {
+          uint32_t p[CH];
+          tmem_ld_cols<CH>(tbase + static_cast<uint32_t>(buf * NT + c), p);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
+            acc[c + j] = fmaf(__uint_as_float(p[j]), s4.x, acc[c + j]);
+            acc[c + j + 1] = fmaf(__uint_as_float(p[j + 1]), s4.y, acc[c + j + 1]);
+            acc[c + j + 2] = fmaf(__uint_as_float(p[j + 2]), s4.z, acc[c + j + 2]);
+            acc[c + j + 3] = fmaf(__uint_as_float(p[j + 3]), s4.w, acc[c + j + 3]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&acce_bar[buf]);
+      }
+      if (!ok) break;
+      const int n = n0 + 32 * q + lane;
+      if (splits > 1) {
+        // the ring is idle: every block has been consumed
+        float* sums = reinterpret_cast<float*>(smem);
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j) sums[(col0 + j) * C::BN + 32 * q + lane] = acc[j];
+      } else if (n < a.N) {
+#pragma unroll
+        for (int j = 0; j < C::COLS; ++j) {
+          const int m = m0 + col0 + j;
+          if (m < a.M) {
+            const size_t o = static_cast<size_t>(m) * a.N + n;
+            float y = acc[j];
+            if (a.residual) y += __bfloat162float(a.residual[o]);
+            a.Y[o] = __float2bfloat16_rn(y);
+          }
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  if (splits > 1) {
+    cluster_sync();  // every CTA's sums are in its shared memory
+    const int m0 = (group % a.m_tiles) * NT, n0 = (group / a.m_tiles) * C::BN;
+    const int rows = min(NT, a.M - m0);
+    const uint32_t sums = smem_u32(smem);
+    // four columns of Y per item, added in the order of the blocks
+    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < rows * (C::BN / 4); i += splits * C::THREADS) {
+      const int j = i / (C::BN / 4), n = n0 + 4 * (i % (C::BN / 4));
+      if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
+      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      for (int r = 0; r < splits; ++r) {
+        const float4 v = ld_shared_cluster_f4(mapa_shared(sums + static_cast<uint32_t>(i) * 16u, r));
+        y[0] += v.x;
+        y[1] += v.y;
+        y[2] += v.z;
+        y[3] += v.w;
+      }
+      const size_t o = static_cast<size_t>(m0 + j) * a.N + n;
+      if (a.residual) {
+        const uint2 rv = *reinterpret_cast<const uint2*>(a.residual + o);
+        y[0] += __uint_as_float(rv.x << 16);
+        y[1] += __uint_as_float(rv.x & 0xFFFF0000u);
+        y[2] += __uint_as_float(rv.y << 16);
+        y[3] += __uint_as_float(rv.y & 0xFFFF0000u);
+      }
+      *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// -------------------------------------------------------------- host side --
+constexpr int kMaxSplits = 8;  // portable cluster size
+
+BlockArgs make_block_args(const BlockLinear& l, int bm, int bn, long long budget) {
+  BlockArgs a;
+  a.sx = l.s_x;
+  a.sw = l.s_w;
+  a.residual = static_cast<const __nv_bfloat16*>(l.residual);
+  a.Y = static_cast<__nv_bfloat16*>(l.Y);
+  a.M = static_cast<int>(l.M);
+  a.N = static_cast<int>(l.N);
+  a.blocks = static_cast<int>((l.K + 127) / 128);
+  a.m_tiles = static_cast<int>((l.M + bm - 1) / bm);
+  a.n_tiles = static_cast<int>((l.N + bn - 1) / bn);
+  a.units = a.m_tiles * a.n_tiles;
+  a.budget = budget;
+  return a;
+}
+
+bool make_block_maps(const BlockLinear& l, uint32_t x_rows, CUtensorMap* tx, CUtensorMap* tw) {
+  const uint64_t k = static_cast<uint64_t>(l.K);
+  return make_map(tx, l.xq, k, static_cast<uint64_t>(l.M), k, x_rows) &&
+         make_map(tw, l.wq, k, static_cast<uint64_t>(l.N), k, 128);
+}
+
+// Clusters of `size` CTAs of a kernel that the current device holds at once
+// (cached per device; 0 when the query fails).
+template <typename K>
+int clusters_resident(K kern, int size, int threads, int smem, std::atomic<int> (&cache)[kMaxDevices]) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return 0;
+  int n = cache[dev].load(std::memory_order_relaxed);
+  if (n > 0) return n - 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned int>(size));
+  cfg.blockDim = dim3(static_cast<unsigned int>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned int>(size);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 0) {
+    cudaGetLastError();
+    n = 0;
+  }
+  cache[dev].store(n + 1, std::memory_order_relaxed);
+  return n;
+}
+
+int pair_clusters() {
+  static std::atomic<int> cache[kMaxDevices];
+  const int n = clusters_resident(gemm_block_pair_kernel, 2, PairTile::THREADS, PairTile::SMEM_BYTES, cache);
+  return n > 0 ? n : 1;
+}
+
+template <int NT>
+int cols_clusters(int splits) {
+  using C = ColsTile<NT>;
+  static std::atomic<int> cache[kMaxSplits + 1][kMaxDevices];
+  return clusters_resident(gemm_block_cols_kernel<NT>, splits, C::THREADS, C::SMEM_BYTES, cache[splits]);
+}
+
+cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t s) {
+  using C = PairTile;
+  CUtensorMap tx, tw;
+  if (!make_block_maps(l, 128, &tx, &tw)) return cudaErrorInvalidValue;
+  const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
+  const cudaError_t e =
+      cudaFuncSetAttribute(gemm_block_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int resident = pair_clusters();
+  const int pairs = a.units < resident ? a.units : resident;
+  return launch_pdl(gemm_block_pair_kernel, dim3(static_cast<unsigned int>(2 * pairs)), dim3(C::THREADS),
+                    C::SMEM_BYTES, s, tx, tw, a);
+}
+
+// CTAs that share a tile: as many as keep every cluster resident at once, at
+// least two blocks of K each.
+template <int NT>
+int cols_splits(int64_t tiles, int64_t blocks) {
+  for (int splits = kMaxSplits; splits > 1; --splits)
+    if (blocks >= 2 * splits && tiles <= cols_clusters<NT>(splits)) return splits;
+  return 1;
+}
+
+template <int NT>
+cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t s) {
+  using C = ColsTile<NT>;
+  CUtensorMap tx, tw;
+  if (!make_block_maps(l, NT, &tx, &tw)) return cudaErrorInvalidValue;
+  const BlockArgs a = make_block_args(l, NT, C::BN, budget);
+  const int splits = cols_splits<NT>(a.units, a.blocks);
+  const int sms = device_sm_count();
+  auto kern = gemm_block_cols_kernel<NT>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  if (splits == 1)
+    return launch_pdl(kern, dim3(static_cast<unsigned int>(a.units < sms ? a.units : sms)), dim3(C::THREADS),
+                      C::SMEM_BYTES, s, tx, tw, a, 1);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned int>(a.units * splits)), dim3(C::THREADS), splits,
+                            C::SMEM_BYTES, s, tx, tw, a, splits);
+}
+
+}  // namespace
+
+cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s) {
+  if (l.M <= 16) return run_block_cols<16>(l, budget, s);
+  if (l.M <= 32) return run_block_cols<32>(l, budget, s);
+  if (l.M <= 64) return run_block_cols<64>(l, budget, s);
+  if (l.M <= 128) return run_block_cols<128>(l, budget, s);
+  const int64_t pair_units = ((l.M + 255) / 256) * ((l.N + 255) / 256);
+  if (pair_units * 2 > device_sm_count() / 2) return run_block_pair(l, budget, s);
+  return run_block_cols<128>(l, budget, s);
+}
+
+cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_block_status, sizeof(unsigned int), 0,
+                                            cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_vlaq_block_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
+  if (e != cudaSuccess) return e;
+  return cudaStreamSynchronize(s);
+}
+
+}  // namespace vlaq

@@ -85,9 +85,43 @@ cudaError_t launch_linear(bool fp4, const uint8_t* xq, const uint8_t* xs, const 
                           void* workspace, size_t ws_bytes, const GemmPlan& plan,
                           long long wait_budget, cudaStream_t s);
 
-// Device status word accessors (gemm.cu, quant.cu).
+// ---- FP8 with block scales of 128 (block128.cu, gemm_block.cu)
+cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, const void* gamma, float eps,
+                                       uint32_t flags, uint8_t* codes, float* s_x, cudaStream_t s);
+cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
+                                          float* s_w, cudaStream_t s);
+struct BlockLinear {
+  const uint8_t* xq;
+  const float* s_x;
+  const uint8_t* wq;
+  const float* s_w;
+  const void* residual;
+  void* Y;
+  int64_t M, N, K;
+};
+cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s);
+struct ResidualNorm {
+  const void* H;
+  const void* Y;
+  int64_t M, K;
+  const void* gamma_post;  // null: no post norm
+  const void* gate;        // null: none
+  int64_t gate_rows;
+  float alpha;
+  const void* gamma_pre;
+  float eps;
+  uint32_t flags;
+  void* H_out;
+  void* X_out;     // bf16 output (null: none)
+  uint8_t* codes;  // FP8 block output (null: the bf16 form)
+  float* s_x;
+};
+cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s);
+
+// Device status word accessors (gemm.cu, quant.cu, gemm_block.cu).
 cudaError_t read_and_clear_status(unsigned int* out, cudaStream_t s);
 cudaError_t read_and_clear_quant_status(unsigned int* out, cudaStream_t s);
+cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s);
 cudaError_t launch_selftest_wait_timeout(cudaStream_t s);
 
 // Kernel launch with the programmatic-stream-serialization attribute, so the
@@ -106,6 +140,27 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The same with thread-block clusters of `cluster` CTAs along x.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int cluster, size_t smem,
+                               cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned int>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

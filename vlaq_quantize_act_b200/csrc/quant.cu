@@ -31,11 +31,12 @@
 //
 // Every quotient x / S is the correctly rounded one (Markstein's
 // correction step after a product with the correctly rounded reciprocal,
-// see quotients() below), so the codes equal those of a plain division.
+// see quotients() in quant_math.cuh), so the codes equal those of a plain division.
 #include <cuda_bf16.h>
 
 #include "internal.h"
 #include "ptx.cuh"
+#include "quant_math.cuh"
 
 namespace vlaq {
 
@@ -65,15 +66,6 @@ struct RowCfg {
   static constexpr int min_blocks(bool bounded) { return (W == 4 && BPL == 2 && bounded) ? 7 : 1; }
 };
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& q, float* v) {
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[2 * j] = __uint_as_float(w[j] << 16);
-    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-  }
-}
-
 // max |x| of 16 bf16 values (two 16-byte words), exact: kept packed as
 // bf16 pairs, the max of bf16 values is one of them.
 __device__ __forceinline__ float absmax_bf16x16(const uint4& a, const uint4& b) {
@@ -89,72 +81,6 @@ __device__ __forceinline__ float absmax_bf16x16(const uint4& a, const uint4& b) 
 #pragma unroll
     for (int j = 0; j < s; ++j) h[j] = __hmax2(h[j], h[j + s]);
   return fmaxf(__low2float(h[0]), __high2float(h[0]));
-}
-
-// Correctly rounded quotient without a divide per element: Markstein's
-// correction step (P. Markstein, "IA-64 and Elementary Functions", 2000:
-// with y = RN(1/S) and q0 = RN(x y), the residual x - q0 S is exact under a
-// fused multiply-add and RN(q0 + (x - q0 S) y) = RN(x / S)).  The residual
-// is formed negated, e' = q0 S - x, so that x = -0 still yields -0.  The
-// reciprocal is CUDA's correctly rounded __frcp_rn, once per divisor.  Only
-// divisors far from 1 (where the residual or 1/S could leave the normal
-// range) and S = 0 take the slow path, behind a warp vote.
-struct Divisor {
-  float S, y;
-  bool slow;  // S = 0 (quotients 0) or S outside [2^-64, 2^64]
-};
-
-__device__ __forceinline__ Divisor make_divisor(float S) {
-  Divisor d;
-  d.S = S;
-  const bool ok = S >= 0x1p-64f && S <= 0x1p64f;
-  d.y = ok ? __frcp_rn(S) : 0.0f;
-  d.slow = !ok;
-  return d;
-}
-
-__device__ __forceinline__ float markstein_quotient(float x, float S, float y) {
-  const float q0 = __fmul_rn(x, y);
-  const float e = __fmaf_rn(q0, S, -x);  // q0 S - x, exact
-  return __fmaf_rn(-e, y, q0);
-}
-
-// RN(v[i] / S) for N values (0 when S = 0).  Executed by the whole warp.
-template <int N>
-__device__ __forceinline__ void quotients(const float* v, const Divisor& d, float* q) {
-  static_assert(N % 2 == 0, "pairs");
-  // the same three steps on packed pairs (sm_100a fp32x2 multiply and fused
-  // multiply-add, each lane rounded once): q0 = x y, e = q0 S - x (x negated
-  // exactly, so -0 stays -0), q = q0 + e (-y)
-  const float2 yy = make_float2(d.y, d.y);
-  const float2 ny = make_float2(-d.y, -d.y);
-  const float2 ss = make_float2(d.S, d.S);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const float2 x = make_float2(v[i], v[i + 1]);
-    const float2 q0 = __fmul2_rn(x, yy);
-    const float2 e = __ffma2_rn(q0, ss, make_float2(-x.x, -x.y));
-    const float2 r = __ffma2_rn(e, ny, q0);
-    q[i] = r.x;
-    q[i + 1] = r.y;
-  }
-  if (__any_sync(0xffffffffu, d.slow)) {
-    if (d.slow) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) q[i] = (d.S == 0.0f) ? 0.0f : __fdiv_rn(v[i], d.S);
-    }
-  }
-}
-
-// The global scale of a row from its amax A >= 0: RN(A / 2688) (NVFP4),
-// RN(A / 448) (FP8) or RN(A / 127) (INT8), by the correction step against
-// the constant's correctly rounded reciprocal; rows whose amax is tiny
-// (quotient near the subnormal range) take a divide.  Uniform per row.
-template <int FMT>
-__device__ __forceinline__ float row_global(float A) {
-  constexpr float c = (FMT == 0) ? 2688.0f : (FMT == 1) ? 448.0f : 127.0f;
-  if (A < 0x1p-64f) return __fdiv_rn(A, c);
-  return markstein_quotient(A, c, __frcp_rn(c));
 }
 
 // E4M3 byte of RN(a / d) for a >= 0 (d is warp-uniform).

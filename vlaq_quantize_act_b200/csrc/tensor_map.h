@@ -1,0 +1,14 @@
+// TMA descriptors of packed codes (gemm.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+
+namespace vlaq {
+
+// 2-D byte tensor [rows, row_bytes] with the given pitch, box 128 x box_rows,
+// 128-byte swizzle, zero fill out of bounds.  False when it cannot be encoded.
+bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
+              uint32_t box_rows);
+
+}  // namespace vlaq
