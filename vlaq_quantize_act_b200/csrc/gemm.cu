@@ -1730,8 +1730,6 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-namespace {
-
 // bf16 output [rows, cols] for TMA tile stores: box 64 columns x 32 rows
 // (128-byte rows), 128-byte swizzle.  Needs a 16-byte aligned base and
 // cols % 8 == 0.
@@ -1746,6 +1744,8 @@ bool make_out_map(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows) {
              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // Packed codes [rows, pitch bytes] viewed as [pitch / 128 chunks][rows][128
 // bytes] for 3-D boxes of 128 bytes x box_rows x box_chunks, 128-byte swizzle

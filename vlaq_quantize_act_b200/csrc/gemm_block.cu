@@ -58,13 +58,15 @@ __device__ __forceinline__ void give_up(volatile int* abort_flag) {
 }
 
 // Bounded wait that also gives up once another role (or, in a pair, a role of
-// the other CTA: peer_abort != 0) aborted.
+// the other CTA: peer_abort != 0) aborted.  The wait sleeps in the barrier
+// unit: polling it cost 225 W of the GPU's 1000 W, which its clock pays for
+// (4580 x 3584 x 18944: 417 -> 411 us).
 __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, long long budget,
                                              volatile int* abort_flag, uint32_t peer_abort) {
   if (mbar_try_wait(bar, parity)) return true;
   const long long t0 = clock64();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (mbar_try_wait_long(bar, parity)) return true;
     if (*abort_flag) return false;
     if (clock64() - t0 > budget) {
       give_up(abort_flag);
@@ -78,14 +80,6 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, lon
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long budget, volatile int* abort_flag,
                                           uint32_t peer_abort) {
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, budget, abort_flag, peer_abort));
-}
-
-// acc[j] += p[j] s for 32 columns, two per instruction.
-__device__ __forceinline__ void add_scaled32(float2* acc, const uint32_t (&p)[32], float s) {
-  const float2 ss = make_float2(s, s);
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    acc[j] = __ffma2_rn(make_float2(__uint_as_float(p[2 * j]), __uint_as_float(p[2 * j + 1])), ss, acc[j]);
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
@@ -102,20 +96,36 @@ __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
 // on the 16 epilogue warps that have read block i - 2 out of its buffer, and
 // one commit per block to both CTAs' done barrier tells the producers that the
 // stage is free and the epilogue warps that the block's sums are there.
-//   warp 0: producer; warp 1: TMEM allocator (both) and MMA issuer (leader);
-//   warps 2, 3: idle; warps 4-11: epilogue, warp e = w - 4 has TMEM lanes
-//   32 (w % 4) .. + 31 (its token rows) and columns 128 (e / 4) .. + 127 (one
-//   weight scale per block).
+//   warps 0, 2: producers of x and w; warp 1: TMEM allocator (both) and MMA
+//   issuer (leader); warp 3: idle; warps 4-11: epilogue, warp e = w - 4 has
+//   TMEM lanes 32 (w % 4) .. + 31 (its token rows) and columns 128 (e / 4) ..
+//   + 127 (one weight scale per block).
 // The sums take 128 registers per epilogue thread: warps 0-3 give theirs up
 // (40), warps 4-11 take 232: 40 + 2 * 232 = 3 * 168 (the build checks that
 // ptxas allocates 168 at entry).
+//
+// What bounds it: the board's 1000 W.  1024 x 37888 x 3584 takes 148 us (1.88
+// PFLOP/s) at 1.43 GHz, 4580 x 3584 x 18944 348 us (1.79) at 1.46 GHz; the
+// per-row FP8 kernel, whose sums stay in TMEM, 131 and 298 us at 1.3 GHz, and
+// this kernel without its epilogue 285 us.  A block takes about 850 clocks of
+// which the MMA is 512: the rest is the round trip from commit to the epilogue
+// warps and back (about 420 clocks by itself) and the 32768 products of a
+// block (281 clocks of the SM's packed multiply-add pipe), less what two
+// buffers overlap.  Measured against this split: 16 epilogue warps of 64
+// columns 172 / 380 us (more instructions per product), MMAs of 128 columns
+// with a barrier for each half 170 / 399 us (twice the round trips).
 struct PairTile {
   static constexpr int BM = 256, BN = 256;
   static constexpr int STAGE_BYTES = 2 * kTileBytes;
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 4;
   static constexpr int EPI_WARPS = 8;
+  static constexpr int AHEAD = 4;                    // blocks a scale is fetched ahead
+  static constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of an epilogue warp
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  static constexpr int REGS_ROLES = 40, REGS_EPI = 232;
+  static_assert(REGS_ROLES + EPI_WARPS / 4 * REGS_EPI == (1 + EPI_WARPS / 4) * 168, "register split");
+  static constexpr int OUT_BYTES = 32 * 128;         // 32 rows x 64 bf16 columns of an epilogue warp
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * 2 * OUT_BYTES + 1024;
   // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = 256, M = 256
   static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -123,12 +133,15 @@ struct PairTile {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTile::THREADS, 1)
 gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
                        const BlockArgs a) {
   using C = PairTile;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[C::STAGES];  // leader: operands of both CTAs, buffer read
   __shared__ __align__(8) uint64_t done_bar[C::STAGES];  // block accumulated (leader's commit)
+  __shared__ __align__(8) uint64_t res_bar[C::EPI_WARPS];  // residual of the warp's part of the tile
   __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ float s_sx[C::AHEAD][32 * C::EPI_WARPS];  // each epilogue thread's own copies of its row's scales
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -143,6 +156,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       mbar_init(&full_bar[i], 1 + 2 * C::EPI_WARPS);
       mbar_init(&done_bar[i], 1);
     }
+    for (int i = 0; i < C::EPI_WARPS; ++i) mbar_init(&res_bar[i], 1);
     mbar_init(&drain_bar, 1);
     s_abort = 0;
     fence_mbarrier_init();
@@ -150,6 +164,8 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmX);
     prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmY);
+    if (a.residual) prefetch_tensormap(&tmR);
   }
   if (warp == 1) {
     tmem_alloc_pair(&s_tmem_base, kTmemColumns);
@@ -161,32 +177,33 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&s_abort)), rank ^ 1u);
+  const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0u);
   griddep_wait();
   griddep_launch_dependents();
 
   if (warp < 4) {
-    regs_dec<40>();
-    if (warp == 0 && lane == 0) {
-      // ----------------------------------------------------------- producer
-      int it = 0;
+    regs_dec<C::REGS_ROLES>();
+    if ((warp == 0 || warp == 2) && elect_one()) {
+      // ---------------------------------------- producers (both CTAs): x, w
+      const bool is_x = warp == 0;
+      const CUtensorMap* map = is_x ? &tmX : &tmW;
+      uint8_t* dst = smem + (is_x ? 0 : kTileBytes);
+      int it = 0, stage = 0;
+      uint32_t phase = 0;
       bool ok = true;
-      uint32_t armed_phase = 0;  // per stage: parity of the last armed phase
       for (int u = pair; u < a.units && ok; u += pairs) {
-        const int m0 = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank);
-        const int n0 = (u / a.m_tiles) * C::BN + 128 * static_cast<int>(rank);
+        const int row0 = (is_x ? (u % a.m_tiles) * C::BM : (u / a.m_tiles) * C::BN) + 128 * static_cast<int>(rank);
         for (int b = 0; b < a.blocks; ++b, ++it) {
-          const int stage = it % C::STAGES;
-          const uint32_t phase = static_cast<uint32_t>(it / C::STAGES) & 1u;
           if (it >= C::STAGES && !bounded_wait(&done_bar[stage], phase ^ 1u, a.budget, &s_abort, peer_abort)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE_BYTES);
-          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          uint8_t* sx = smem + stage * C::STAGE_BYTES;
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0u);
-          tma_load_2d_pair(sx, &tmX, bar, b * kRowBytes, m0);
-          tma_load_2d_pair(sx + kTileBytes, &tmW, bar, b * kRowBytes, n0);
+          if (is_x && rank == 0) mbar_arrive_expect_tx(&full_bar[stage], 2 * C::STAGE_BYTES);
+          tma_load_2d_pair(dst + stage * C::STAGE_BYTES, map, leader_full + 8u * stage, b * kRowBytes, row0);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
       if (ok) {
@@ -194,38 +211,36 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
           bounded_wait(&done_bar[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, a.budget, &s_abort,
                        peer_abort);
-      } else if (rank == 0) {
-        // let every load in flight land before the pair's final barrier
-        for (int i = 0; i < C::STAGES && i < it; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&full_bar[i], (armed_phase >> i) & 1u) && clock64() - t0 < (1ll << 21)) {
-          }
-        }
       } else {
-        // the peer cannot observe the leader's barriers: time instead
+        // a stage that was given up may never complete: give every copy in
+        // flight the time to land before the pair's final barrier
         const long long t0 = clock64();
         while (clock64() - t0 < (1ll << 21)) {
         }
       }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0 && elect_one()) {
       // ------------------------------------------------- MMA issuer (leader)
-      int it = 0;
+      const uint64_t xd = sdesc_kmajor_sw128(smem_u32(smem)), wd = sdesc_kmajor_sw128(smem_u32(smem) + kTileBytes);
+      int stage = 0;
+      uint32_t phase = 0, buf = 0;
       bool ok = true;
       for (int u = pair; u < a.units && ok; u += pairs) {
-        for (int b = 0; b < a.blocks; ++b, ++it) {
-          const int stage = it % C::STAGES;
-          if (!bounded_wait(&full_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort,
-                            peer_abort)) {
+        for (int b = 0; b < a.blocks; ++b) {
+          if (!bounded_wait(&full_bar[stage], phase, a.budget, &s_abort, peer_abort)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES), b0 = a0 + kTileBytes;
-          const uint32_t d = tmem + static_cast<uint32_t>((it & 1) * C::BN);
+          const uint64_t off = static_cast<uint64_t>(stage) * (C::STAGE_BYTES >> 4);  // descriptor units of 16 bytes
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            mma_f8f6f4_pair(d, sdesc_kmajor_sw128(a0 + 32 * j), sdesc_kmajor_sw128(b0 + 32 * j), C::IDESC, j > 0);
+            mma_f8f6f4_pair(tmem + buf, xd + off + 2 * j, wd + off + 2 * j, C::IDESC, j > 0);
           umma_commit_pair(&done_bar[stage], 0x3);
+          buf ^= C::BN;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
       umma_commit_pair(&drain_bar, 0x1);
@@ -235,101 +250,131 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     }
   } else {
     // ------------------------------------------------- epilogue (both CTAs)
-    regs_inc<232>();
+    regs_inc<C::REGS_EPI>();
     const int q = warp & 3;
     const int h = (warp - 4) >> 2;
-    auto buffer_read = [&](int block) {  // this warp is done with the buffer that block reuses
+    auto buffer_read = [&](int stage) {  // this warp has read the buffer that the block of that stage reuses
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full_bar[block % C::STAGES]), 0u));
+      if (lane == 0) mbar_arrive_cluster_relaxed(leader_full + 8u * stage);
     };
     buffer_read(0);
     buffer_read(1);
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(128 * h);
-    int it = 0;
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(C::COLS * h);
+    uint8_t* out = smem + C::STAGES * C::STAGE_BYTES + (warp - 4) * 2 * C::OUT_BYTES;
+    uint32_t res_phase = 0;
+    bool loading = false;  // a residual load in flight
+    int stage = 0;
+    const uint32_t ring = smem_u32(&s_sx[0][threadIdx.x - 128]);
+    uint32_t phase = 0, buf = 0;
     bool ok = true;
     for (int u = pair; u < a.units && ok; u += pairs) {
-      const int row = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank) + 32 * q + lane;
-      const int col0 = (u / a.m_tiles) * C::BN + 128 * h;
-      const bool live = row < a.M && col0 < a.N;
-      // scales of four blocks at a time, the next four in flight meanwhile
-      const float* sxp = a.sx + row;
-      const float* swp = a.sw + static_cast<int64_t>(col0 >> 7) * a.blocks;
-      auto scale = [&](int b) {
-        return live && b < a.blocks ? __ldg(sxp + static_cast<int64_t>(b) * a.M) * __ldg(swp + b) : 0.0f;
+      const int row0 = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank) + 32 * q;
+      const int col0 = (u / a.m_tiles) * C::BN + C::COLS * h;
+      const bool live = row0 < a.M && col0 < a.N;  // warp-uniform
+      if (a.residual && lane == 0) {
+        // the residual lands in the staging buffer while the blocks are summed;
+        // the previous tile's stores have read it by then
+        bulk_wait_group_read0();
+        mbar_arrive_expect_tx(&res_bar[warp - 4], 2 * C::OUT_BYTES);
+        tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
+        tma_load_2d(out + C::OUT_BYTES, &tmR, &res_bar[warp - 4], col0 + 64, row0);
+      }
+      loading = a.residual != nullptr;
+      // Row scales come through this thread's own ring in shared memory, four
+      // blocks ahead (asynchronous copies: a load held in a register makes the
+      // warp wait for it where the register moves on); weight scales 32 blocks
+      // at a time, one per lane.  Rows and columns past the output use the
+      // last ones' scales and are not stored.
+      const float* sxp = a.sx + min(row0 + lane, a.M - 1);
+      const float* swp = a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks;
+      auto fetch = [&](int b) {
+        if (b < a.blocks) cp_async4(ring + (b % C::AHEAD) * (128 * C::EPI_WARPS), sxp + static_cast<int64_t>(b) * a.M);
+        cp_async_commit();
       };
-      float2 acc[64];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
-      float next[4];
+      for (int i = 0; i < C::AHEAD; ++i) fetch(i);
+      float w32 = 0.0f, w32n = __ldg(swp + min(lane, a.blocks - 1));
+      float acc[C::COLS];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) next[t] = scale(t);
-      for (int b0 = 0; b0 < a.blocks && ok; b0 += 4) {
-        float cur[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          cur[t] = next[t];
-          next[t] = scale(b0 + 4 + t);
+      for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+      for (int b = 0; b < a.blocks; ++b) {
+        if ((b & 31) == 0) {
+          w32 = w32n;
+          w32n = __ldg(swp + min(b + 32 + lane, a.blocks - 1));
         }
+        cp_async_wait<C::AHEAD - 1>();
+        const float sc = s_sx[b % C::AHEAD][threadIdx.x - 128] * __shfl_sync(0xffffffffu, w32, b & 31);
+        fetch(b + C::AHEAD);
+        if (!warp_wait(&done_bar[stage], phase, a.budget, &s_abort, peer_abort)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // one load at a time: the scheduler's other epilogue warps compute
+        // meanwhile
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (b0 + t >= a.blocks) break;
-          const int stage = it % C::STAGES;
-          if (!warp_wait(&done_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort,
-                         peer_abort)) {
-            ok = false;
-            break;
+        for (int c = 0; c < C::COLS; c += 32) {
+          uint32_t p[32];
+          tmem_ld_32x32b_x32(tbase + buf + c, p);
+          tmem_ld_wait();
+          if (c + 32 == C::COLS) buffer_read(stage + 2 < C::STAGES ? stage + 2 : stage + 2 - C::STAGES);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float2 r = __ffma2_rn(make_float2(__uint_as_float(p[j]), __uint_as_float(p[j + 1])),
+                                        make_float2(sc, sc), make_float2(acc[c + j], acc[c + j + 1]));
+            acc[c + j] = r.x;
+            acc[c + j + 1] = r.y;
           }
-          tc_fence_after();
-          const uint32_t tb = tbase + static_cast<uint32_t>((it & 1) * C::BN);
-          uint32_t p0[32], p1[32];
-          tmem_ld_32x32b_x32(tb, p0);
-          tmem_ld_wait();
-          tmem_ld_32x32b_x32(tb + 32, p1);
-          add_scaled32(acc, p0, cur[t]);
-          tmem_ld_wait();
-          tmem_ld_32x32b_x32(tb + 64, p0);
-          add_scaled32(acc + 16, p1, cur[t]);
-          tmem_ld_wait();
-          tmem_ld_32x32b_x32(tb + 96, p1);
-          add_scaled32(acc + 32, p0, cur[t]);
-          tmem_ld_wait();
-          buffer_read(it + 2);
-          add_scaled32(acc + 48, p1, cur[t]);
-          ++it;
+        }
+        buf ^= C::BN;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
       if (!ok) break;
-      if (live) {
-        const size_t base = static_cast<size_t>(row) * a.N + col0;
-        __nv_bfloat16* yp = a.Y + base;
-        const __nv_bfloat16* rp = a.residual ? a.residual + base : nullptr;
+      // + residual, bf16, through the staging buffer (128-byte rows in the
+      // copy engine's 128-byte swizzle) and out by tile stores, which clip
+      // rows and columns past the output; the next tile's sums start meanwhile
+      if (a.residual) {
+        if (!warp_wait(&res_bar[warp - 4], res_phase, a.budget, &s_abort, peer_abort)) break;
+        res_phase ^= 1u;
+        loading = false;
+      } else {
+        if (lane == 0) bulk_wait_group_read0();
+        __syncwarp();
+      }
 #pragma unroll
-        for (int g = 0; g < 16; ++g) {  // 8 columns each; N % 8 == 0: in or out as a whole
-          if (col0 + 8 * g < a.N) {
-            float y[8];
+      for (int c = 0; c < C::COLS; c += 8) {
+        const uint32_t at = smem_u32(out) + (c / 64) * C::OUT_BYTES + lane * 128 + ((((c / 8) & 7) ^ (lane & 7)) << 4);
+        if (a.residual) {
+          const uint4 rv = ld_shared_v4(at);
+          const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              y[2 * j] = acc[4 * g + j].x;
-              y[2 * j + 1] = acc[4 * g + j].y;
-            }
-            if (rp) {
-              const uint4 rv = *reinterpret_cast<const uint4*>(rp + 8 * g);
-              const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                y[2 * j] += __uint_as_float(rw[j] << 16);
-                y[2 * j + 1] += __uint_as_float(rw[j] & 0xFFFF0000u);
-              }
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = bf16x2(y[2 * j], y[2 * j + 1]);
-            *reinterpret_cast<uint4*>(yp + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int j = 0; j < 4; ++j) {
+            acc[c + 2 * j] += __uint_as_float(rw[j] << 16);
+            acc[c + 2 * j + 1] += __uint_as_float(rw[j] & 0xFFFF0000u);
           }
         }
+        st_shared_v4(at, bf16x2(acc[c], acc[c + 1]), bf16x2(acc[c + 2], acc[c + 3]), bf16x2(acc[c + 4], acc[c + 5]),
+                     bf16x2(acc[c + 6], acc[c + 7]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && live) {
+        tma_store_2d(&tmY, out, col0, row0);
+        if (col0 + 64 < a.N) tma_store_2d(&tmY, out + C::OUT_BYTES, col0 + 64, row0);
+        bulk_commit_group();
       }
     }
+    if (loading) {
+      // the tile was given up: let its residual land before teardown
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&res_bar[warp - 4], res_phase) && clock64() - t0 < (1ll << 21)) {
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
   }
 
   // Neither CTA leaves (or frees its TMEM) while the other may still signal
@@ -702,8 +747,11 @@ int cols_clusters(int splits) {
 
 cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t s) {
   using C = PairTile;
-  CUtensorMap tx, tw;
-  if (!make_block_maps(l, 128, &tx, &tw)) return cudaErrorInvalidValue;
+  CUtensorMap tx, tw, ty, tr;
+  const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
+  if (!make_block_maps(l, 128, &tx, &tw) || !make_out_map(&ty, l.Y, cols, rows)) return cudaErrorInvalidValue;
+  tr = ty;  // not read without a residual
+  if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
   const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
   const cudaError_t e =
       cudaFuncSetAttribute(gemm_block_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
@@ -711,7 +759,7 @@ cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t 
   const int resident = pair_clusters();
   const int pairs = a.units < resident ? a.units : resident;
   return launch_pdl(gemm_block_pair_kernel, dim3(static_cast<unsigned int>(2 * pairs)), dim3(C::THREADS),
-                    C::SMEM_BYTES, s, tx, tw, a);
+                    C::SMEM_BYTES, s, tx, tw, ty, tr, a);
 }
 
 // CTAs that share a tile: as many as keep every cluster resident at once, at

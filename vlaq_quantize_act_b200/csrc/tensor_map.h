@@ -11,4 +11,8 @@ namespace vlaq {
 bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t rows, uint64_t pitch,
               uint32_t box_rows);
 
+// bf16 tensor [rows, cols] in tiles of 64 columns x 32 rows (128-byte rows),
+// 128-byte swizzle.  Needs a 16-byte aligned base and cols % 8 == 0.
+bool make_out_map(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows);
+
 }  // namespace vlaq
