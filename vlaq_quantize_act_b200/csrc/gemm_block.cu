@@ -82,9 +82,91 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, budget, abort_flag, peer_abort));
 }
 
+// acc[j] += p[j] s for 32 columns, two per instruction.
+__device__ __forceinline__ void add_scaled32(float* acc, const uint32_t (&p)[32], float s) {
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const float2 r = __ffma2_rn(make_float2(__uint_as_float(p[j]), __uint_as_float(p[j + 1])), make_float2(s, s),
+                                make_float2(acc[j], acc[j + 1]));
+    acc[j] = r.x;
+    acc[j + 1] = r.y;
+  }
+}
+
+// Scales s_x s_w of n consecutive blocks for an epilogue thread's row and
+// weight block.  The row's scales come through the thread's own ring of four
+// slots in shared memory, copied four blocks ahead (a load into a register
+// makes the warp wait for it where the register moves on: with the next
+// block's scale in a register every block took an L2 round trip), the
+// weight's 32 blocks at a time, one per lane.
+constexpr int kScaleSlots = 4;
+template <int THREADS>  // epilogue threads: distance of a thread's slots
+struct ScaleStream {
+  const float* sx;  // the row's scale of block 0; M apart from the next
+  const float* sw;
+  int n;
+  float* slots;
+  float w, w_next;
+
+  __device__ __forceinline__ void copy(int i, int M) {
+    if (i < n) cp_async4(smem_u32(slots + (i % kScaleSlots) * THREADS), sx + static_cast<int64_t>(i) * M);
+    cp_async_commit();
+  }
+  __device__ __forceinline__ void start(const float* row_scales, const float* weight_scales, int blocks,
+                                        float* thread_slots, int M, int lane) {
+    sx = row_scales;
+    sw = weight_scales;
+    n = blocks;
+    slots = thread_slots;
+    w_next = __ldg(sw + min(lane, n - 1));
+#pragma unroll
+    for (int i = 0; i < kScaleSlots; ++i) copy(i, M);
+  }
+  // The scale of block i; called for i = 0, 1, ...
+  __device__ __forceinline__ float next(int i, int M, int lane) {
+    if ((i & 31) == 0) {
+      w = w_next;
+      w_next = __ldg(sw + min(i + 32 + lane, n - 1));
+    }
+    cp_async_wait<kScaleSlots - 1>();
+    const float s = slots[(i % kScaleSlots) * THREADS] * __shfl_sync(0xffffffffu, w, i & 31);
+    copy(i + kScaleSlots, M);
+    return s;
+  }
+};
+
 __device__ __forceinline__ uint32_t bf16x2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Barrier over the epilogue warps (`threads` threads).  All of them reach it
+// the same number of times whatever happens: a warp whose wait ran out skips
+// its work, not its barriers.
+__device__ __forceinline__ void epilogue_sync(int threads) {
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
+// Y[m, n .. n + 3] = bf16(sum over the cluster's CTAs, in rank order, of the
+// four fp32 sums at shared address `at` + residual).
+__device__ __forceinline__ void store_summed4(const BlockArgs& a, uint32_t at, int ctas, int m, int n) {
+  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int r = 0; r < ctas; ++r) {
+    const float4 v = ld_shared_cluster_f4(mapa_shared(at, r));
+    y[0] += v.x;
+    y[1] += v.y;
+    y[2] += v.z;
+    y[3] += v.w;
+  }
+  const size_t o = static_cast<size_t>(m) * a.N + n;
+  if (a.residual) {
+    const uint2 rv = *reinterpret_cast<const uint2*>(a.residual + o);
+    y[0] += __uint_as_float(rv.x << 16);
+    y[1] += __uint_as_float(rv.x & 0xFFFF0000u);
+    y[2] += __uint_as_float(rv.y << 16);
+    y[3] += __uint_as_float(rv.y & 0xFFFF0000u);
+  }
+  *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
 }
 
 // ---------------------------------------------------------------------------
@@ -119,7 +201,6 @@ struct PairTile {
   static constexpr int STAGE_BYTES = 2 * kTileBytes;
   static constexpr int STAGES = 4;
   static constexpr int EPI_WARPS = 8;
-  static constexpr int AHEAD = 4;                    // blocks a scale is fetched ahead
   static constexpr int COLS = BN / (EPI_WARPS / 4);  // columns of an epilogue warp
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
   static constexpr int REGS_ROLES = 40, REGS_EPI = 232;
@@ -141,7 +222,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   __shared__ __align__(8) uint64_t done_bar[C::STAGES];  // block accumulated (leader's commit)
   __shared__ __align__(8) uint64_t res_bar[C::EPI_WARPS];  // residual of the warp's part of the tile
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ float s_sx[C::AHEAD][32 * C::EPI_WARPS];  // each epilogue thread's own copies of its row's scales
+  __shared__ float s_sx[kScaleSlots][32 * C::EPI_WARPS];  // each epilogue thread's own copies of its row's scales
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -265,7 +346,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     uint32_t res_phase = 0;
     bool loading = false;  // a residual load in flight
     int stage = 0;
-    const uint32_t ring = smem_u32(&s_sx[0][threadIdx.x - 128]);
+    float* slots = &s_sx[0][threadIdx.x - 128];
     uint32_t phase = 0, buf = 0;
     bool ok = true;
     for (int u = pair; u < a.units && ok; u += pairs) {
@@ -281,51 +362,27 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         tma_load_2d(out + C::OUT_BYTES, &tmR, &res_bar[warp - 4], col0 + 64, row0);
       }
       loading = a.residual != nullptr;
-      // Row scales come through this thread's own ring in shared memory, four
-      // blocks ahead (asynchronous copies: a load held in a register makes the
-      // warp wait for it where the register moves on); weight scales 32 blocks
-      // at a time, one per lane.  Rows and columns past the output use the
-      // last ones' scales and are not stored.
-      const float* sxp = a.sx + min(row0 + lane, a.M - 1);
-      const float* swp = a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks;
-      auto fetch = [&](int b) {
-        if (b < a.blocks) cp_async4(ring + (b % C::AHEAD) * (128 * C::EPI_WARPS), sxp + static_cast<int64_t>(b) * a.M);
-        cp_async_commit();
-      };
-#pragma unroll
-      for (int i = 0; i < C::AHEAD; ++i) fetch(i);
-      float w32 = 0.0f, w32n = __ldg(swp + min(lane, a.blocks - 1));
+      // rows and columns past the output use the last ones' scales and are not stored
+      ScaleStream<32 * C::EPI_WARPS> scales;
+      scales.start(a.sx + min(row0 + lane, a.M - 1), a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks,
+                   a.blocks, slots, a.M, lane);
       float acc[C::COLS];
 #pragma unroll
       for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
       for (int b = 0; b < a.blocks; ++b) {
-        if ((b & 31) == 0) {
-          w32 = w32n;
-          w32n = __ldg(swp + min(b + 32 + lane, a.blocks - 1));
-        }
-        cp_async_wait<C::AHEAD - 1>();
-        const float sc = s_sx[b % C::AHEAD][threadIdx.x - 128] * __shfl_sync(0xffffffffu, w32, b & 31);
-        fetch(b + C::AHEAD);
+        const float sc = scales.next(b, a.M, lane);
         if (!warp_wait(&done_bar[stage], phase, a.budget, &s_abort, peer_abort)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // one load at a time: the scheduler's other epilogue warps compute
-        // meanwhile
 #pragma unroll
         for (int c = 0; c < C::COLS; c += 32) {
           uint32_t p[32];
           tmem_ld_32x32b_x32(tbase + buf + c, p);
           tmem_ld_wait();
           if (c + 32 == C::COLS) buffer_read(stage + 2 < C::STAGES ? stage + 2 : stage + 2 - C::STAGES);
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float2 r = __ffma2_rn(make_float2(__uint_as_float(p[j]), __uint_as_float(p[j + 1])),
-                                        make_float2(sc, sc), make_float2(acc[c + j], acc[c + j + 1]));
-            acc[c + j] = r.x;
-            acc[c + j + 1] = r.y;
-          }
+          add_scaled32(acc + c, p, sc);
         }
         buf ^= C::BN;
         if (++stage == C::STAGES) {
@@ -389,55 +446,49 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 }
 
 // ---------------------------------------------------------------------------
-// Tile: 128 weight rows (MMA rows, TMEM lanes) x NT tokens (columns).  The
-// CTAs of a cluster share a tile and take consecutive ranges of its blocks; a
-// cluster of one loops over tiles.
-//   warp 0: producer; warp 1: TMEM allocator and MMA issuer; warp 2: scales
-//   (the products s_x s_w of a block, one per column, in shared memory);
-//   warp 3: idle; warps 4 ..: epilogue, warp e = w - 4 has weight rows 32 (w %
-//   4) .. + 31 and columns COLS (e / 4) .. + COLS - 1.
-template <int NT>
-struct ColsTile {
-  static constexpr int BN = 128;  // weight rows
-  static constexpr int X_BYTES = NT * kRowBytes;
-  static constexpr int STAGE_BYTES = kTileBytes + X_BYTES;
-  static constexpr int STAGES = (196 * 1024) / STAGE_BYTES > 10 ? 10 : (196 * 1024) / STAGE_BYTES;
-  static constexpr int BUFS = 4;  // accumulator buffers (and scale slots)
-  static constexpr int EPI_WARPS = NT >= 64 ? 8 : 4;
-  static constexpr int COLS = NT / (EPI_WARPS / 4);
+// One CTA per tile of 128 tokens (TMEM lanes) x 128 weight rows (columns), or
+// a cluster of CTAs that take consecutive ranges of the tile's blocks and add
+// their sums in shared memory; a cluster of one loops over tiles.
+//   warps 0, 2: producers of x and w; warp 1: TMEM allocator and MMA issuer;
+//   warp 3: idle; warps 4-11: epilogue, warp e = w - 4 has tokens 32 (w % 4)
+//   .. + 31 and columns 64 (e / 4) .. + 63.
+// Four accumulator buffers of 128 columns, block i in buffer i % 4; as in the
+// pair kernel the full barrier of block i also waits for the epilogue warps
+// that have read block i - 4.
+struct RowsTile {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int STAGE_BYTES = 2 * kTileBytes;
+  static constexpr int STAGES = 5;
+  static constexpr int BUFS = 4;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int COLS = BN / (EPI_WARPS / 4);
   static constexpr int THREADS = 128 + 32 * EPI_WARPS;
-  static constexpr int TMEM_COLS = BUFS * NT;  // a power of two, >= 32
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
-  // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = NT, M = 128
-  static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(BN >> 4) << 24);
-  static_assert(NT * BN * 4 <= STAGES * STAGE_BYTES, "the cluster's sums fit the operand ring");
-  static_assert(TMEM_COLS <= kTmemColumns, "TMEM budget");
+  static constexpr int OUT_BYTES = 32 * 128;  // 32 rows x 64 bf16 columns of an epilogue warp
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * OUT_BYTES + 1024;
+  // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = 128, M = 128
+  static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+  static_assert(BM * BN * 4 <= STAGES * STAGE_BYTES, "the cluster's sums fit the operand ring");
+  static_assert(BUFS * BN <= kTmemColumns, "TMEM budget");
+  static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-template <int COLS>
-__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[COLS]);
-template <>
-__device__ __forceinline__ void tmem_ld_cols<32>(uint32_t taddr, uint32_t (&r)[32]) {
-  tmem_ld_32x32b_x32(taddr, r);
-}
-template <>
-__device__ __forceinline__ void tmem_ld_cols<16>(uint32_t taddr, uint32_t (&r)[16]) {
-  tmem_ld_32x32b_x16(taddr, r);
+// Column group (16 bytes) c of row r of the cluster's sums: the groups of a
+// row are rotated by the row, so that the 32 rows of a warp fall on all banks.
+__device__ __forceinline__ uint32_t sums_offset(int r, int c) {
+  return static_cast<uint32_t>((r * (RowsTile::BN / 4) + (c ^ (r & 31))) * 16);
 }
 
-template <int NT>
-__global__ void __launch_bounds__(ColsTile<NT>::THREADS, 1)
-gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(RowsTile::THREADS, 1)
+gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
                        const BlockArgs a, const int splits) {
-  using C = ColsTile<NT>;
+  using C = RowsTile;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[C::STAGES];   // operands of a block
-  __shared__ __align__(8) uint64_t empty_bar[C::STAGES];  // block consumed
-  __shared__ __align__(8) uint64_t accf_bar[C::BUFS];     // block accumulated
-  __shared__ __align__(8) uint64_t scf_bar[C::BUFS];      // block's scales written
-  __shared__ __align__(8) uint64_t acce_bar[C::BUFS];     // accumulator and scales read
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];    // operands of a block, buffer read
+  __shared__ __align__(8) uint64_t done_bar[C::STAGES];    // block accumulated
+  __shared__ __align__(8) uint64_t res_bar[C::EPI_WARPS];  // residual of the warp's part of the tile
   __shared__ __align__(8) uint64_t drain_bar;
-  __shared__ __align__(16) float s_scale[C::BUFS][NT];
+  __shared__ float s_sx[kScaleSlots][32 * C::EPI_WARPS];  // each epilogue thread's own copies of its row's scales
   __shared__ uint32_t s_tmem_base;
   __shared__ volatile int s_abort;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -446,18 +497,284 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int group = static_cast<int>(blockIdx.x) / splits;
   const int groups = static_cast<int>(gridDim.x) / splits;
-  const int kb0 = static_cast<int>(static_cast<int64_t>(a.blocks) * rank / splits);
-  const int kb1 = static_cast<int>(static_cast<int64_t>(a.blocks) * (rank + 1) / splits);
+  // blocks <= 2^24, splits <= 8
+  const int kb0 = static_cast<int>(static_cast<uint32_t>(a.blocks * rank) / static_cast<uint32_t>(splits));
+  const int kb1 = static_cast<int>(static_cast<uint32_t>(a.blocks * (rank + 1)) / static_cast<uint32_t>(splits));
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
-      mbar_init(&full_bar[i], 1);
-      mbar_init(&empty_bar[i], 1);
+      mbar_init(&full_bar[i], 1 + C::EPI_WARPS);
+      mbar_init(&done_bar[i], 1);
     }
-    for (int i = 0; i < C::BUFS; ++i) {
-      mbar_init(&accf_bar[i], 1);
-      mbar_init(&scf_bar[i], 1);
-      mbar_init(&acce_bar[i], C::EPI_WARPS);
+    for (int i = 0; i < C::EPI_WARPS; ++i) mbar_init(&res_bar[i], 1);
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmX);
+    prefetch_tensormap(&tmW);
+    prefetch_tensormap(&tmY);
+    if (a.residual) prefetch_tensormap(&tmR);
+  }
+  if (warp == 1) {
+    tmem_alloc(&s_tmem_base, C::BUFS * C::BN);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem_base;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if ((warp == 0 || warp == 2) && elect_one()) {
+    // ----------------------------------------------------- producers: x, w
+    const bool is_x = warp == 0;
+    const CUtensorMap* map = is_x ? &tmX : &tmW;
+    uint8_t* dst = smem + (is_x ? 0 : kTileBytes);
+    int it = 0, stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      const int row0 = is_x ? (u % a.m_tiles) * C::BM : (u / a.m_tiles) * C::BN;
+      for (int b = kb0; b < kb1; ++b, ++it) {
+        if (it >= C::STAGES && !bounded_wait(&done_bar[stage], phase ^ 1u, a.budget, &s_abort, 0)) {
+          ok = false;
+          break;
+        }
+        if (is_x) mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
+        tma_load_2d(dst + stage * C::STAGE_BYTES, map, &full_bar[stage], b * kRowBytes, row0);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      // a stage that was given up may never complete: give every copy in
+      // flight the time to land before teardown
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1ll << 21)) {
+      }
+    }
+  } else if (warp == 1 && elect_one()) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint64_t xd = sdesc_kmajor_sw128(smem_u32(smem)), wd = sdesc_kmajor_sw128(smem_u32(smem) + kTileBytes);
+    int stage = 0;
+    uint32_t phase = 0, buf = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      for (int b = kb0; b < kb1; ++b) {
+        if (!bounded_wait(&full_bar[stage], phase, a.budget, &s_abort, 0)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t off = static_cast<uint64_t>(stage) * (C::STAGE_BYTES >> 4);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          mma_f8f6f4(tmem + buf, xd + off + 2 * j, wd + off + 2 * j, C::IDESC, j > 0);
+        umma_commit(&done_bar[stage]);
+        buf = (buf + C::BN) & (C::BUFS * C::BN - 1);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    umma_commit(&drain_bar);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- epilogue
+    const int q = warp & 3;
+    const int h = (warp - 4) >> 2;
+    auto buffer_read = [&](int stage) {  // this warp has read the buffer that the block of that stage reuses
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&full_bar[stage]);
+    };
+#pragma unroll
+    for (int i = 0; i < C::BUFS; ++i) buffer_read(i);
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(C::COLS * h);
+    float* slots = &s_sx[0][threadIdx.x - 128];
+    uint8_t* out = smem + C::STAGES * C::STAGE_BYTES + (warp - 4) * C::OUT_BYTES;
+    uint32_t res_phase = 0;
+    bool loading = false;  // a residual load in flight
+    int stage = 0;
+    uint32_t phase = 0, buf = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      const int row0 = (u % a.m_tiles) * C::BM + 32 * q;
+      const int col0 = (u / a.m_tiles) * C::BN + C::COLS * h;
+      const bool live = row0 < a.M && col0 < a.N;  // warp-uniform
+      if (a.residual && splits == 1) {
+        if (lane == 0) {
+          bulk_wait_group_read0();
+          mbar_arrive_expect_tx(&res_bar[warp - 4], C::OUT_BYTES);
+          tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
+        }
+        loading = true;
+      }
+      // rows and columns past the output use the last ones' scales and are not stored
+      const int n = kb1 - kb0;
+      ScaleStream<32 * C::EPI_WARPS> scales;
+      scales.start(a.sx + static_cast<int64_t>(kb0) * a.M + min(row0 + lane, a.M - 1),
+                   a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks + kb0, n, slots, a.M, lane);
+      float acc[C::COLS];
+#pragma unroll
+      for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+      float sc = scales.next(0, a.M, lane);
+      bool ready = false;
+      for (int b = 0; b < n; ++b) {
+        if (!__all_sync(0xffffffffu, ready) && !warp_wait(&done_bar[stage], phase, a.budget, &s_abort, 0)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // the next block's scale and barrier and the second load overlap the
+        // first load and the products
+        uint32_t p0[32], p1[32];
+        tmem_ld_32x32b_x32(tbase + buf, p0);
+        const float sc1 = b + 1 < n ? scales.next(b + 1, a.M, lane) : 0.0f;
+        tmem_ld_wait();
+        tmem_ld_32x32b_x32(tbase + buf + 32, p1);
+        add_scaled32(acc, p0, sc);
+        tmem_ld_wait();
+        buffer_read(stage + C::BUFS < C::STAGES ? stage + C::BUFS : stage + C::BUFS - C::STAGES);
+        buf = (buf + C::BN) & (C::BUFS * C::BN - 1);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+        ready = mbar_test_wait(&done_bar[stage], phase);
+        add_scaled32(acc + 32, p1, sc);
+        sc = sc1;
+      }
+      if (!ok) break;
+      if (splits > 1) {
+        // the ring is idle: every block of this CTA's range has been consumed
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 4)
+          st_shared_v4(smem_u32(smem) + sums_offset(32 * q + lane, (C::COLS * h + c) / 4), __float_as_uint(acc[c]),
+                       __float_as_uint(acc[c + 1]), __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3]));
+      } else {
+        if (a.residual) {
+          if (!warp_wait(&res_bar[warp - 4], res_phase, a.budget, &s_abort, 0)) break;
+          res_phase ^= 1u;
+          loading = false;
+        } else {
+          if (lane == 0) bulk_wait_group_read0();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int c = 0; c < C::COLS; c += 8) {
+          const uint32_t at = smem_u32(out) + lane * 128 + (((c / 8) ^ (lane & 7)) << 4);
+          if (a.residual) {
+            const uint4 rv = ld_shared_v4(at);
+            const uint32_t rw[4] = {rv.x, rv.y, rv.z, rv.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              acc[c + 2 * j] += __uint_as_float(rw[j] << 16);
+              acc[c + 2 * j + 1] += __uint_as_float(rw[j] & 0xFFFF0000u);
+            }
+          }
+          st_shared_v4(at, bf16x2(acc[c], acc[c + 1]), bf16x2(acc[c + 2], acc[c + 3]), bf16x2(acc[c + 4], acc[c + 5]),
+                       bf16x2(acc[c + 6], acc[c + 7]));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && live) {
+          tma_store_2d(&tmY, out, col0, row0);
+          bulk_commit_group();
+        }
+      }
+    }
+    if (loading) {
+      // the tile was given up: let its residual land before teardown
+      const long long t0 = clock64();
+      while (!mbar_try_wait(&res_bar[warp - 4], res_phase) && clock64() - t0 < (1ll << 21)) {
+      }
+    }
+    if (lane == 0) bulk_wait_group0();
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  if (splits > 1) {
+    cluster_sync();  // every CTA's sums are in its shared memory
+    const int m0 = (group % a.m_tiles) * C::BM, n0 = (group / a.m_tiles) * C::BN;
+    const int rows = min(C::BM, a.M - m0);
+    const uint32_t sums = smem_u32(smem);
+    // four columns of Y per item, added in the order of the blocks
+    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < rows * (C::BN / 4); i += splits * C::THREADS) {
+      const int j = i / (C::BN / 4), c = i % (C::BN / 4), n = n0 + 4 * c;
+      if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
+      store_summed4(a, sums + sums_offset(j, c), splits, m0 + j, n);
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+  } else {
+    __syncthreads();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::BUFS * C::BN);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Decode: 128 weight rows (MMA rows, TMEM lanes) x NT tokens (columns), so the
+// MMA and the epilogue are as narrow as the tokens and the weights stream
+// once.  Clusters, roles and barriers as in the kernel above, with four
+// epilogue warps; the token scales of kChunk blocks at a time go through
+// shared memory, copied by the epilogue warps one chunk ahead.
+template <int NT>
+struct ColsTile {
+  static constexpr int BN = 128;  // weight rows
+  static constexpr int X_BYTES = NT * kRowBytes;
+  static constexpr int STAGE_BYTES = kTileBytes + X_BYTES;
+  static constexpr int STAGES = (192 * 1024) / STAGE_BYTES > 10 ? 10 : (192 * 1024) / STAGE_BYTES;
+  static constexpr int BUFS = 4;  // accumulator buffers
+  static constexpr int CHUNK = 8;  // blocks of scales per copy
+  static constexpr int EPI_WARPS = 4;
+  static constexpr int THREADS = 128 + 32 * EPI_WARPS;
+  static constexpr int TMEM_COLS = BUFS * NT;  // a power of two, >= 32
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024;
+  // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = NT, M = 128
+  static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(NT >> 3) << 17) | (uint32_t(BN >> 4) << 24);
+  static_assert(NT * BN * 4 <= STAGES * STAGE_BYTES, "the cluster's sums fit the operand ring");
+  static_assert(BUFS < STAGES, "a stage's barrier is armed after its buffer's previous block");
+  static_assert(TMEM_COLS <= kTmemColumns, "TMEM budget");
+};
+
+template <int NT>
+__global__ void __launch_bounds__(ColsTile<NT>::THREADS, 1)
+gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                       const BlockArgs a, const int splits) {
+  using C = ColsTile<NT>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[C::STAGES];  // operands of a block, buffer read
+  __shared__ __align__(8) uint64_t done_bar[C::STAGES];  // block accumulated
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(16) float s_sx[2][C::CHUNK][NT];  // token scales of two chunks of blocks
+  __shared__ uint32_t s_tmem_base;
+  __shared__ volatile int s_abort;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int group = static_cast<int>(blockIdx.x) / splits;
+  const int groups = static_cast<int>(gridDim.x) / splits;
+  // blocks <= 2^24, splits <= 8
+  const int kb0 = static_cast<int>(static_cast<uint32_t>(a.blocks * rank) / static_cast<uint32_t>(splits));
+  const int kb1 = static_cast<int>(static_cast<uint32_t>(a.blocks * (rank + 1)) / static_cast<uint32_t>(splits));
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::STAGES; ++i) {
+      mbar_init(&full_bar[i], 1 + C::EPI_WARPS);
+      mbar_init(&done_bar[i], 1);
     }
     mbar_init(&drain_bar, 1);
     s_abort = 0;
@@ -478,156 +795,151 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   griddep_wait();
   griddep_launch_dependents();
 
-  if (warp == 0) {
-    // ------------------------------------------------------------- producer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      uint32_t armed_phase = 0;
-      for (int u = group; u < a.units && ok; u += groups) {
-        const int m0 = (u % a.m_tiles) * NT, n0 = (u / a.m_tiles) * C::BN;
-        for (int b = kb0; b < kb1; ++b, ++it) {
-          const int stage = it % C::STAGES;
-          const uint32_t phase = static_cast<uint32_t>(it / C::STAGES) & 1u;
-          if (!bounded_wait(&empty_bar[stage], phase ^ 1u, a.budget, &s_abort, 0)) {
-            ok = false;
-            break;
-          }
-          mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
-          armed_phase = (armed_phase & ~(1u << stage)) | (phase << stage);
-          uint8_t* sw = smem + stage * C::STAGE_BYTES;
-          tma_load_2d(sw, &tmW, &full_bar[stage], b * kRowBytes, n0);
-          tma_load_2d(sw + kTileBytes, &tmX, &full_bar[stage], b * kRowBytes, m0);
-        }
-      }
-      if (!ok) {
-        // let every load in flight land before teardown
-        for (int i = 0; i < C::STAGES && i < it; ++i) {
-          const long long t0 = clock64();
-          while (!mbar_try_wait(&full_bar[i], (armed_phase >> i) & 1u) && clock64() - t0 < a.budget) {
-          }
-        }
-      }
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (int u = group; u < a.units && ok; u += groups) {
-        for (int b = kb0; b < kb1; ++b, ++it) {
-          const int stage = it % C::STAGES, buf = it % C::BUFS;
-          if (!bounded_wait(&acce_bar[buf], (static_cast<uint32_t>(it / C::BUFS) & 1u) ^ 1u, a.budget, &s_abort, 0) ||
-              !bounded_wait(&full_bar[stage], static_cast<uint32_t>(it / C::STAGES) & 1u, a.budget, &s_abort, 0)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t w0 = smem_u32(smem + stage * C::STAGE_BYTES), x0 = w0 + kTileBytes;
-          const uint32_t d = tmem + static_cast<uint32_t>(buf * NT);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mma_f8f6f4(d, sdesc_kmajor_sw128(w0 + 32 * j), sdesc_kmajor_sw128(x0 + 32 * j), C::IDESC, j > 0);
-          umma_commit(&empty_bar[stage]);
-          umma_commit(&accf_bar[buf]);
-        }
-      }
-      umma_commit(&drain_bar);
-      const long long t0 = clock64();
-      while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
-      }
-    }
-  } else if (warp == 2) {
-    // --------------------------------------------------------------- scales
-    constexpr int PER_LANE = (NT + 31) / 32;
-    int it = 0;
+  if ((warp == 0 || warp == 2) && elect_one()) {
+    // ----------------------------------------------------- producers: w, x
+    const bool is_w = warp == 0;
+    const CUtensorMap* map = is_w ? &tmW : &tmX;
+    uint8_t* dst = smem + (is_w ? 0 : kTileBytes);
+    int it = 0, stage = 0;
+    uint32_t phase = 0;
     bool ok = true;
     for (int u = group; u < a.units && ok; u += groups) {
-      const int m0 = (u % a.m_tiles) * NT, nb = u / a.m_tiles;
-      const float* swp = a.sw + static_cast<int64_t>(nb) * a.blocks;
-      constexpr int AHEAD = 4;  // blocks loaded ahead of use
-      float next[AHEAD][PER_LANE];
-      auto load = [&](int b, float (&s)[PER_LANE]) {
-        const float w = b < kb1 ? __ldg(swp + b) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) {
-          const int m = m0 + lane + 32 * i;
-          s[i] = b < kb1 && lane + 32 * i < NT && m < a.M ? w * __ldg(a.sx + static_cast<int64_t>(b) * a.M + m) : 0.0f;
-        }
-      };
-#pragma unroll
-      for (int t = 0; t < AHEAD; ++t) load(kb0 + t, next[t]);
-      for (int b0 = kb0; b0 < kb1 && ok; b0 += AHEAD) {
-#pragma unroll
-        for (int t = 0; t < AHEAD; ++t) {
-          if (b0 + t >= kb1) break;
-          const int buf = it % C::BUFS;
-          if (!warp_wait(&acce_bar[buf], (static_cast<uint32_t>(it / C::BUFS) & 1u) ^ 1u, a.budget, &s_abort, 0)) {
-            ok = false;
-            break;
-          }
-#pragma unroll
-          for (int i = 0; i < PER_LANE; ++i)
-            if (lane + 32 * i < NT) s_scale[buf][lane + 32 * i] = next[t][i];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&scf_bar[buf]);
-          load(b0 + AHEAD + t, next[t]);
-          ++it;
-        }
-      }
-    }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------- epilogue
-    constexpr int CH = C::COLS < 32 ? C::COLS : 32;  // columns per TMEM load
-    const int q = warp & 3;
-    const int col0 = ((warp - 4) >> 2) * C::COLS;
-    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(col0);
-    int it = 0;
-    bool ok = true;
-    for (int u = group; u < a.units && ok; u += groups) {
-      const int m0 = (u % a.m_tiles) * NT, n0 = (u / a.m_tiles) * C::BN;
-      float acc[C::COLS];
-#pragma unroll
-      for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
+      const int row0 = is_w ? (u / a.m_tiles) * C::BN : (u % a.m_tiles) * NT;
       for (int b = kb0; b < kb1; ++b, ++it) {
-        const int buf = it % C::BUFS;
-        const uint32_t phase = static_cast<uint32_t>(it / C::BUFS) & 1u;
-        if (!warp_wait(&scf_bar[buf], phase, a.budget, &s_abort, 0) ||
-            !warp_wait(&accf_bar[buf], phase, a.budget, &s_abort, 0)) {
+        if (it >= C::STAGES && !bounded_wait(&done_bar[stage], phase ^ 1u, a.budget, &s_abort, 0)) {
+          ok = false;
+          break;
+        }
+        if (is_w) mbar_arrive_expect_tx(&full_bar[stage], C::STAGE_BYTES);
+        tma_load_2d(dst + stage * C::STAGE_BYTES, map, &full_bar[stage], b * kRowBytes, row0);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (!ok) {
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1ll << 21)) {
+      }
+    }
+  } else if (warp == 1 && elect_one()) {
+    // ----------------------------------------------------------- MMA issuer
+    const uint64_t wd = sdesc_kmajor_sw128(smem_u32(smem)), xd = sdesc_kmajor_sw128(smem_u32(smem) + kTileBytes);
+    int stage = 0;
+    uint32_t phase = 0, buf = 0;
+    bool ok = true;
+    for (int u = group; u < a.units && ok; u += groups) {
+      for (int b = kb0; b < kb1; ++b) {
+        if (!bounded_wait(&full_bar[stage], phase, a.budget, &s_abort, 0)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const float* sc = &s_scale[buf][col0];
+        const uint64_t off = static_cast<uint64_t>(stage) * (C::STAGE_BYTES >> 4);
 #pragma unroll
-        for (int c = 0; c < C::COLS; c += CH) {
-          uint32_t p[CH];
-          tmem_ld_cols<CH>(tbase + static_cast<uint32_t>(buf * NT + c), p);
-          tmem_ld_wait();
+        for (int j = 0; j < 4; ++j)
+          mma_f8f6f4(tmem + buf, wd + off + 2 * j, xd + off + 2 * j, C::IDESC, j > 0);
+        umma_commit(&done_bar[stage]);
+        buf = (buf + NT) & (C::TMEM_COLS - 1);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    umma_commit(&drain_bar);
+    const long long t0 = clock64();
+    while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------- epilogue
+    constexpr int CH = NT < 32 ? NT : 32;  // columns per TMEM load
+    const int q = warp & 3;
+    const int t = static_cast<int>(threadIdx.x) - 128;
+    auto buffer_read = [&](int stage) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_relaxed(&full_bar[stage]);
+    };
 #pragma unroll
-          for (int j = 0; j < CH; j += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(sc + c + j);
-            acc[c + j] = fmaf(__uint_as_float(p[j]), s4.x, acc[c + j]);
-            acc[c + j + 1] = fmaf(__uint_as_float(p[j + 1]), s4.y, acc[c + j + 1]);
-            acc[c + j + 2] = fmaf(__uint_as_float(p[j + 2]), s4.z, acc[c + j + 2]);
-            acc[c + j + 3] = fmaf(__uint_as_float(p[j + 3]), s4.w, acc[c + j + 3]);
+    for (int i = 0; i < C::BUFS; ++i) buffer_read(i);
+    const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16);
+    int stage = 0;
+    uint32_t phase = 0, buf = 0;
+    bool ok = true;
+    for (int u = group; u < a.units; u += groups) {
+      const int m0 = (u % a.m_tiles) * NT, n0 = (u / a.m_tiles) * C::BN;
+      const float* swp = a.sw + static_cast<int64_t>(u / a.m_tiles) * a.blocks;
+      // columns past the last token use its scales and are not stored
+      auto copy_chunk = [&](int b, int half) {
+        for (int i = t; i < C::CHUNK * NT; i += 32 * C::EPI_WARPS)
+          if (b + i / NT < kb1)
+            cp_async4(smem_u32(&s_sx[half][0][i]), a.sx + static_cast<int64_t>(b + i / NT) * a.M + min(m0 + i % NT, a.M - 1));
+        cp_async_commit();
+      };
+      copy_chunk(kb0, 0);
+      float w8 = 0.0f, w8n = __ldg(swp + min(kb0 + lane, a.blocks - 1));  // weight scales, one per lane
+      float acc[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[j] = 0.0f;
+      int half = 0;
+      for (int b0 = kb0; b0 < kb1; b0 += C::CHUNK) {
+        w8 = w8n;
+        w8n = __ldg(swp + min(b0 + C::CHUNK + lane, a.blocks - 1));
+        cp_async_wait<0>();
+        // every warp's part of this chunk has landed, and the other chunk's
+        // buffer has been read by all
+        epilogue_sync(32 * C::EPI_WARPS);
+        copy_chunk(b0 + C::CHUNK, half ^ 1);
+        const int b1 = min(b0 + C::CHUNK, kb1);
+        for (int b = b0; b < b1 && ok; ++b) {
+          const float w = __shfl_sync(0xffffffffu, w8, b - b0);
+          if (!warp_wait(&done_bar[stage], phase, a.budget, &s_abort, 0)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const float4* sc = reinterpret_cast<const float4*>(&s_sx[half][b - b0][0]);
+#pragma unroll
+          for (int c = 0; c < NT; c += CH) {
+            uint32_t p[CH];
+            if constexpr (CH == 32)
+              tmem_ld_32x32b_x32(tbase + buf + c, p);
+            else
+              tmem_ld_32x32b_x16(tbase + buf + c, p);
+            tmem_ld_wait();
+            if (c + CH == NT) buffer_read(stage + C::BUFS < C::STAGES ? stage + C::BUFS : stage + C::BUFS - C::STAGES);
+#pragma unroll
+            for (int j = 0; j < CH; j += 4) {
+              const float4 s4 = sc[(c + j) / 4];
+              acc[c + j] = fmaf(__uint_as_float(p[j]), s4.x * w, acc[c + j]);
+              acc[c + j + 1] = fmaf(__uint_as_float(p[j + 1]), s4.y * w, acc[c + j + 1]);
+              acc[c + j + 2] = fmaf(__uint_as_float(p[j + 2]), s4.z * w, acc[c + j + 2]);
+              acc[c + j + 3] = fmaf(__uint_as_float(p[j + 3]), s4.w * w, acc[c + j + 3]);
+            }
+          }
+          buf = (buf + NT) & (C::TMEM_COLS - 1);
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1u;
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&acce_bar[buf]);
+        half ^= 1;
       }
-      if (!ok) break;
+      cp_async_wait<0>();
+      epilogue_sync(32 * C::EPI_WARPS);  // the next tile's first chunk overwrites this tile's last
       const int n = n0 + 32 * q + lane;
+      if (!ok) continue;
       if (splits > 1) {
         // the ring is idle: every block has been consumed
         float* sums = reinterpret_cast<float*>(smem);
 #pragma unroll
-        for (int j = 0; j < C::COLS; ++j) sums[(col0 + j) * C::BN + 32 * q + lane] = acc[j];
+        for (int j = 0; j < NT; ++j) sums[j * C::BN + 32 * q + lane] = acc[j];
       } else if (n < a.N) {
 #pragma unroll
-        for (int j = 0; j < C::COLS; ++j) {
-          const int m = m0 + col0 + j;
+        for (int j = 0; j < NT; ++j) {
+          const int m = m0 + j;
           if (m < a.M) {
             const size_t o = static_cast<size_t>(m) * a.N + n;
             float y = acc[j];
@@ -650,23 +962,7 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < rows * (C::BN / 4); i += splits * C::THREADS) {
       const int j = i / (C::BN / 4), n = n0 + 4 * (i % (C::BN / 4));
       if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
-      float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int r = 0; r < splits; ++r) {
-        const float4 v = ld_shared_cluster_f4(mapa_shared(sums + static_cast<uint32_t>(i) * 16u, r));
-        y[0] += v.x;
-        y[1] += v.y;
-        y[2] += v.z;
-        y[3] += v.w;
-      }
-      const size_t o = static_cast<size_t>(m0 + j) * a.N + n;
-      if (a.residual) {
-        const uint2 rv = *reinterpret_cast<const uint2*>(a.residual + o);
-        y[0] += __uint_as_float(rv.x << 16);
-        y[1] += __uint_as_float(rv.x & 0xFFFF0000u);
-        y[2] += __uint_as_float(rv.y << 16);
-        y[3] += __uint_as_float(rv.y & 0xFFFF0000u);
-      }
-      *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
+      store_summed4(a, sums + static_cast<uint32_t>(i) * 16u, splits, m0 + j, n);
     }
     cluster_sync();  // no CTA leaves while another reads its sums
   } else {
@@ -738,11 +1034,39 @@ int pair_clusters() {
   return n > 0 ? n : 1;
 }
 
+int rows_clusters(int splits) {
+  using C = RowsTile;
+  static std::atomic<int> cache[kMaxSplits + 1][kMaxDevices];
+  return clusters_resident(gemm_block_rows_kernel, splits, C::THREADS, C::SMEM_BYTES, cache[splits]);
+}
+
 template <int NT>
 int cols_clusters(int splits) {
   using C = ColsTile<NT>;
   static std::atomic<int> cache[kMaxSplits + 1][kMaxDevices];
   return clusters_resident(gemm_block_cols_kernel<NT>, splits, C::THREADS, C::SMEM_BYTES, cache[splits]);
+}
+
+// CTAs that share a tile: as many as keep every cluster resident at once, at
+// least two blocks of K each.
+template <typename Resident>
+int choose_splits(int64_t tiles, int64_t blocks, Resident resident) {
+  for (int splits = kMaxSplits; splits > 1; --splits)
+    if (blocks >= 2 * splits && tiles <= resident(splits)) return splits;
+  return 1;
+}
+
+// Tiles of one CTA each (grid capped at the SMs, which loop), or of a cluster.
+template <typename Kernel, typename... Args>
+cudaError_t launch_tiles(Kernel kern, int threads, int smem, int units, int splits, cudaStream_t s, Args... args) {
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int sms = device_sm_count();
+  if (splits == 1)
+    return launch_pdl(kern, dim3(static_cast<unsigned int>(units < sms ? units : sms)), dim3(threads), smem, s,
+                      args..., 1);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned int>(units * splits)), dim3(threads), splits, smem, s,
+                            args..., splits);
 }
 
 cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t s) {
@@ -762,13 +1086,16 @@ cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t 
                     C::SMEM_BYTES, s, tx, tw, ty, tr, a);
 }
 
-// CTAs that share a tile: as many as keep every cluster resident at once, at
-// least two blocks of K each.
-template <int NT>
-int cols_splits(int64_t tiles, int64_t blocks) {
-  for (int splits = kMaxSplits; splits > 1; --splits)
-    if (blocks >= 2 * splits && tiles <= cols_clusters<NT>(splits)) return splits;
-  return 1;
+cudaError_t run_block_rows(const BlockLinear& l, long long budget, cudaStream_t s) {
+  using C = RowsTile;
+  CUtensorMap tx, tw, ty, tr;
+  const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
+  if (!make_block_maps(l, C::BM, &tx, &tw) || !make_out_map(&ty, l.Y, cols, rows)) return cudaErrorInvalidValue;
+  tr = ty;  // not read without a residual
+  if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
+  const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
+  return launch_tiles(gemm_block_rows_kernel, C::THREADS, C::SMEM_BYTES, a.units,
+                      choose_splits(a.units, a.blocks, rows_clusters), s, tx, tw, ty, tr, a);
 }
 
 template <int NT>
@@ -777,16 +1104,8 @@ cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t 
   CUtensorMap tx, tw;
   if (!make_block_maps(l, NT, &tx, &tw)) return cudaErrorInvalidValue;
   const BlockArgs a = make_block_args(l, NT, C::BN, budget);
-  const int splits = cols_splits<NT>(a.units, a.blocks);
-  const int sms = device_sm_count();
-  auto kern = gemm_block_cols_kernel<NT>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  if (splits == 1)
-    return launch_pdl(kern, dim3(static_cast<unsigned int>(a.units < sms ? a.units : sms)), dim3(C::THREADS),
-                      C::SMEM_BYTES, s, tx, tw, a, 1);
-  return launch_pdl_cluster(kern, dim3(static_cast<unsigned int>(a.units * splits)), dim3(C::THREADS), splits,
-                            C::SMEM_BYTES, s, tx, tw, a, splits);
+  return launch_tiles(gemm_block_cols_kernel<NT>, C::THREADS, C::SMEM_BYTES, a.units,
+                      choose_splits(a.units, a.blocks, cols_clusters<NT>), s, tx, tw, a);
 }
 
 }  // namespace
@@ -795,10 +1114,9 @@ cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cuda
   if (l.M <= 16) return run_block_cols<16>(l, budget, s);
   if (l.M <= 32) return run_block_cols<32>(l, budget, s);
   if (l.M <= 64) return run_block_cols<64>(l, budget, s);
-  if (l.M <= 128) return run_block_cols<128>(l, budget, s);
   const int64_t pair_units = ((l.M + 255) / 256) * ((l.N + 255) / 256);
   if (pair_units * 2 > device_sm_count() / 2) return run_block_pair(l, budget, s);
-  return run_block_cols<128>(l, budget, s);
+  return run_block_rows(l, budget, s);
 }
 
 cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s) {
