@@ -104,6 +104,9 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():
+            # the raw handle: building a Stream object took 3.9 us of a 9 us call
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
