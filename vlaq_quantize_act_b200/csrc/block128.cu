@@ -41,6 +41,19 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float* v) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// max |v| of 8 bf16 values, kept packed (the max of bf16 values is one of them).
+__device__ __forceinline__ float absmax_bf16x8(const uint4& a) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t aw = w[j] & 0x7FFF7FFFu;  // |x| of both halves
+    h[j] = *reinterpret_cast<const __nv_bfloat162*>(&aw);
+  }
+  const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
 __device__ __forceinline__ float absmax8(const float* v) {
   float m = 0.0f;
 #pragma unroll
@@ -94,6 +107,15 @@ __device__ __forceinline__ float block_scale16(const float* v) {
 #pragma unroll
   for (int x = 1; x < 16; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   return row_global<1>(m);
+}
+
+// Largest of all threads' values (>= 0).  Executed by the whole CTA.
+__device__ __forceinline__ float block_amax(float m, float* s_max) {
+  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // bit order is value order
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = m;
+  __syncthreads();
+  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); ++w) m = fmaxf(m, s_max[w]);
+  return m;
 }
 
 // ------------------------------------------------------ activation blocks --
@@ -150,60 +172,178 @@ __global__ void __launch_bounds__(kBlocksThreads) quant_blocks_kernel(const Bloc
 
 // ------------------------------------------------------------ weight blocks --
 // One CTA per 128 x 128 block: 16 lanes cover a row's 128 columns, 16 rows at
-// a time; the whole block stays in registers (8 chunks per thread) between
-// the amax and the codes, so W is read once.
+// a time; the whole block stays in registers (8 chunks of bf16 per thread)
+// between the amax and the codes, so W is read once.  HBM-bound: 37888 x 3584
+// in 63.5 us, 6.42 TB/s (64 registers, four CTAs per SM; with the 104 of an
+// unbounded build, two CTAs, 85 us; with 40, spilled, 96 us).
 constexpr int kWeightThreads = 256;
 
-template <bool WHT>
-__global__ void __launch_bounds__(kWeightThreads) quant_weight_block_kernel(const __nv_bfloat16* W, int64_t N,
-                                                                             int64_t K, uint8_t* codes,
-                                                                             float* scales) {
+__global__ void __launch_bounds__(kWeightThreads, 4)
+    quant_weight_block_kernel(const __nv_bfloat16* W, int64_t N, int64_t K, uint8_t* codes, float* scales) {
   __shared__ float s_max[kWeightThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4, lane = threadIdx.x & 31;
-  const int64_t k_blocks = (K + 127) / 128;
+  const int sub = threadIdx.x & 15, r0 = threadIdx.x >> 4;
+  const uint32_t k_blocks = static_cast<uint32_t>((K + 127) / 128);
   const int64_t nb = blockIdx.x / k_blocks, kb = blockIdx.x % k_blocks;
   const int64_t k = kb * 128 + 8 * sub;
+  const int64_t first = (nb * 128 + r0) * K + k;  // this thread's first chunk, 16 rows to the next
+  const int rows = static_cast<int>(min(static_cast<int64_t>(128), N - nb * 128));
   uint4 d[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t n = nb * 128 + r0 + 16 * i;
-    d[i] = n < N && k < K ? __ldg(reinterpret_cast<const uint4*>(W + n * K + k)) : make_uint4(0, 0, 0, 0);
-  }
-  float v[WHT ? 8 : 1][8];
+  for (int i = 0; i < 8; ++i)
+    d[i] = r0 + 16 * i < rows && k < K ? __ldg(reinterpret_cast<const uint4*>(W + first + 16 * i * K))
+                                       : make_uint4(0, 0, 0, 0);
   float m = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float t[8];
-    unpack_bf16x8(d[i], t);
-    if (WHT) {
-      wht64_chunk(t, lane);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = t[j];
-    }
-    m = fmaxf(m, absmax8(t));
-  }
-  m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));  // m >= 0: bit order is value order
-  if (lane == 0) s_max[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWeightThreads / 32; ++w) m = fmaxf(m, s_max[w]);
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, absmax_bf16x8(d[i]));
+  m = block_amax(m, s_max);
   const float s = row_global<1>(m);
   const Divisor dv = make_divisor(s);
   if (threadIdx.x == 0) scales[blockIdx.x] = s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     float t[8];
-    if (WHT) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = v[i][j];
-    } else {
-      unpack_bf16x8(d[i], t);
-    }
+    unpack_bf16x8(d[i], t);
     const uint2 w = e4m3_codes8(t, dv);
-    const int64_t n = nb * 128 + r0 + 16 * i;
-    if (n < N && k < K) *reinterpret_cast<uint2*>(codes + n * K + k) = w;
+    if (r0 + 16 * i < rows && k < K) *reinterpret_cast<uint2*>(codes + first + 16 * i * K) = w;
+  }
+}
+
+// ------------------------------------------------- rotated blocks, many rows --
+// Rotations of plain bf16 input (weights, activations without a norm): a
+// thread transforms one whole 64-element block in its registers, so nothing
+// is exchanged between lanes (with the block over 8 lanes, 24 shuffles per 8
+// elements bound the kernel: 37888 x 3584 in 131 us).  A CTA takes 128 units of 128
+// elements at a time, the rows of a 128 x 128 weight block or 128 consecutive
+// 1 x 128 activation blocks; they come into shared memory by asynchronous
+// copies, one tile ahead, and lanes 2 i and 2 i + 1 read the halves of a unit.
+// 16-byte group c of unit u lies at group (c & 8) + ((c ^ u ^ c / 2 & 4) & 7),
+// which puts the eight lanes of each read phase on different banks.
+constexpr int kRotThreads = 256;
+constexpr int kRotUnits = kRotThreads / 2;
+constexpr int kRotTileBytes = kRotUnits * 256;
+constexpr int kRotSmem = 2 * kRotTileBytes;
+
+__device__ __forceinline__ uint32_t rot_offset(int unit, int c) {
+  return static_cast<uint32_t>(unit * 256 + ((c & 8) + ((c ^ unit ^ ((c >> 1) & 4)) & 7)) * 16);
+}
+
+// Unnormalised WHT of 64 values (8 times the normalised one), stages in the
+// sequential order, each sum and difference rounded once; the packed stages
+// as in wht64_lanes.
+__device__ __forceinline__ void wht64_thread(float2 (&v)[32]) {
+  const float2 m1 = make_float2(-1.0f, -1.0f);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = make_float2(__fadd_rn(v[i].x, v[i].y), __fsub_rn(v[i].x, v[i].y));
+#pragma unroll
+  for (int h = 1; h < 32; h <<= 1) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if ((i & h) == 0) {
+        const float2 a = v[i], b = v[i + h];
+        v[i] = __fadd2_rn(a, b);
+        v[i + h] = __ffma2_rn(b, m1, a);
+      }
+    }
+  }
+}
+
+struct RotArgs {
+  const __nv_bfloat16* X;
+  int64_t rows, K;
+  int64_t k_blocks;
+  int64_t tiles;
+  unsigned long long inv_blocks;  // floor(2^64 / k_blocks) + 1 (k_blocks > 1)
+  uint8_t* codes;
+  float* scales;
+};
+
+// Row and column of unit u of a tile, row < 0 past the data.
+template <bool WEIGHT>
+__device__ __forceinline__ void rot_unit(const RotArgs& a, int64_t tile, int u, int64_t& row, int64_t& col) {
+  if (WEIGHT) {
+    const int64_t nb = a.k_blocks == 1 ? tile : static_cast<int64_t>(__umul64hi(tile, a.inv_blocks));
+    row = nb * 128 + u;
+    col = (tile - nb * a.k_blocks) * 128;
+  } else {
+    const int64_t i = tile * kRotUnits + u;
+    row = a.k_blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
+    col = (i - row * a.k_blocks) * 128;
+  }
+  if (row >= a.rows) row = -1;
+}
+
+template <bool WEIGHT>
+__global__ void __launch_bounds__(kRotThreads, 2) quant_rotated_kernel(const RotArgs a) {
+  extern __shared__ __align__(128) uint8_t s_tiles[];
+  __shared__ float s_max[kRotThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t base = smem_u32(s_tiles);
+  // 16 lanes copy a unit; what lies past the data is filled with zeros
+  auto copy = [&](int64_t tile, int buf) {
+    if (tile < a.tiles) {
+      const int c = threadIdx.x & 15;
+#pragma unroll
+      for (int u = threadIdx.x >> 4; u < kRotUnits; u += kRotThreads / 16) {
+        int64_t row, col;
+        rot_unit<WEIGHT>(a, tile, u, row, col);
+        const bool in = row >= 0 && col + 8 * c < a.K;
+        cp_async16(base + buf * kRotTileBytes + rot_offset(u, c), in ? a.X + row * a.K + col + 8 * c : a.X, in);
+      }
+    }
+    cp_async_commit();
+  };
+  const int unit = threadIdx.x >> 1, half = threadIdx.x & 1;
+  copy(blockIdx.x, 0);
+  int buf = 0;
+  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, buf ^= 1) {
+    copy(tile + gridDim.x, buf ^ 1);
+    cp_async_wait<1>();
+    __syncthreads();
+    float2 v[32];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 q = ld_shared_v4(base + buf * kRotTileBytes + rot_offset(unit, 8 * half + c));
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[4 * c + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+    }
+    wht64_thread(v);
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) m = fmaxf(m, fmaxf(fabsf(v[i].x), fabsf(v[i].y)));
+    // the transform's factor 1/8, exact here (sums of bf16 values are
+    // multiples of 2^-133), goes into the amax and the divisor
+    m = __fmul_rn(m, 0.125f);
+    if (WEIGHT)
+      m = block_amax(m, s_max);
+    else
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const float s = row_global<1>(m);
+    const Divisor dv = make_divisor(__fmul_rn(s, 8.0f));
+    int64_t row, col;
+    rot_unit<WEIGHT>(a, tile, unit, row, col);
+    const bool in = row >= 0 && col + 64 * half < a.K;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t[8] = {v[4 * i].x,     v[4 * i].y,     v[4 * i + 1].x, v[4 * i + 1].y,
+                          v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y};
+      const uint2 q = e4m3_codes8(t, dv);
+      w[2 * i] = q.x;
+      w[2 * i + 1] = q.y;
+    }
+    if (in) {
+      uint4* dst = reinterpret_cast<uint4*>(a.codes + row * a.K + col + 64 * half);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+      if (!WEIGHT && half == 0) a.scales[(col >> 7) * a.rows + row] = s;
+    }
+    if (WEIGHT && threadIdx.x == 0) a.scales[tile] = s;
+    __syncthreads();  // the buffer (and s_max) have been read
   }
 }
 
@@ -371,6 +511,19 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   return launch_norm_shape<RESID, WHT, OUT, 256, 16>(a, s);
 }
 
+// Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64.
+constexpr int64_t kFewBlocks = 8192;
+
+template <bool WEIGHT>
+cudaError_t launch_rotated(const RotArgs& r, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(quant_rotated_kernel<WEIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kRotSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t ctas = 2 * static_cast<int64_t>(device_sm_count());
+  return launch_pdl(quant_rotated_kernel<WEIGHT>, dim3(static_cast<unsigned int>(r.tiles < ctas ? r.tiles : ctas)),
+                    dim3(kRotThreads), kRotSmem, s, r);
+}
+
 }  // namespace
 
 cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, const void* gamma, float eps,
@@ -387,13 +540,21 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
     a.K = static_cast<int>(K);
     return wht ? launch_norm<false, true, kOutFp8>(a, s) : launch_norm<false, false, kOutFp8>(a, s);
   }
+  const int64_t blocks = (K + 127) / 128;
+  const unsigned long long inv = blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(blocks) + 1;
+  // Few rotated blocks finish sooner spread over 8 lanes each: see launch_rotated
+  if (wht && M * blocks > kFewBlocks) {
+    RotArgs r = {static_cast<const __nv_bfloat16*>(X), M, K, blocks, (M * blocks + kRotUnits - 1) / kRotUnits, inv,
+                 codes, s_x};
+    return launch_rotated<false>(r, s);
+  }
   BlocksArgs a;
   a.X = static_cast<const __nv_bfloat16*>(X);
   a.rows = M;
   a.K = K;
-  a.blocks = (K + 127) / 128;
-  a.total = M * a.blocks;
-  a.inv_blocks = a.blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(a.blocks) + 1;
+  a.blocks = blocks;
+  a.total = M * blocks;
+  a.inv_blocks = inv;
   a.codes = codes;
   a.scales = s_x;
   const int64_t grid = (a.total + kUnroll * kGroups - 1) / (kUnroll * kGroups);
@@ -404,10 +565,14 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
 
 cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
                                           float* s_w, cudaStream_t s) {
-  const int64_t grid = ((N + 127) / 128) * ((K + 127) / 128);
-  if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl((flags & kFlagHadamard) ? quant_weight_block_kernel<true> : quant_weight_block_kernel<false>,
-                    dim3(static_cast<unsigned int>(grid)), dim3(kWeightThreads), 0, s,
+  const int64_t blocks = (K + 127) / 128, tiles = ((N + 127) / 128) * blocks;
+  if (flags & kFlagHadamard) {
+    const unsigned long long inv = blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(blocks) + 1;
+    RotArgs r = {static_cast<const __nv_bfloat16*>(W), N, K, blocks, tiles, inv, codes, s_w};
+    return launch_rotated<true>(r, s);
+  }
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return launch_pdl(quant_weight_block_kernel, dim3(static_cast<unsigned int>(tiles)), dim3(kWeightThreads), 0, s,
                     static_cast<const __nv_bfloat16*>(W), N, K, codes, s_w);
 }
 
