@@ -136,6 +136,9 @@ vlaq_status vlaq_check(void* stream) {
   e = vlaq::read_and_clear_block_status(&bst, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
   st |= bst;
+  e = vlaq::read_and_clear_block128_status(&bst, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
+  st |= bst;
   if (st & vlaq::kStatusTimeout) {
     // a GEMM that gave up may have left split-K tile counters non-zero
     e = vlaq::noalloc_clear(static_cast<cudaStream_t>(stream));

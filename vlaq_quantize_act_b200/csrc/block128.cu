@@ -24,8 +24,11 @@
 #include "internal.h"
 #include "ptx.cuh"
 #include "quant_math.cuh"
+#include "tensor_map.h"
 
 namespace vlaq {
+
+__device__ unsigned int g_vlaq_block128_status = 0;
 
 namespace {
 
@@ -93,14 +96,6 @@ __device__ __forceinline__ void wht64_chunk(float* v, int lane) {
   for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], 0.125f);
 }
 
-// Codes of 8 values of a block with divisor d: two words, element 0 lowest.
-__device__ __forceinline__ uint2 e4m3_codes8(const float* v, const Divisor& d) {
-  float q[8];
-  quotients<8>(v, d, q);
-  return make_uint2(cvt_e4m3x2(q[0], q[1]) | (cvt_e4m3x2(q[2], q[3]) << 16),
-                    cvt_e4m3x2(q[4], q[5]) | (cvt_e4m3x2(q[6], q[7]) << 16));
-}
-
 // Scale of the 1 x 128 block on 16 adjacent lanes.  Executed by the warp.
 __device__ __forceinline__ float block_scale16(const float* v) {
   float m = absmax8(v);
@@ -119,8 +114,7 @@ __device__ __forceinline__ float block_amax(float m, float* s_max) {
 }
 
 // ------------------------------------------------------ activation blocks --
-// Without a norm the blocks of all rows are independent: 16 lanes take one
-// block, kUnroll blocks each with their loads in flight together.
+// Without a norm the blocks of all rows are independent.
 struct BlocksArgs {
   const __nv_bfloat16* X;
   int64_t rows, K;
@@ -131,42 +125,64 @@ struct BlocksArgs {
   float* scales;                   // [blocks][rows]
 };
 
-constexpr int kBlocksThreads = 256;
-constexpr int kUnroll = 4;
-constexpr int kGroups = kBlocksThreads / 16;
+// Row of block i: exact while i * blocks < 2^64.
+__device__ __forceinline__ int64_t block_row(const BlocksArgs& a, int64_t i) {
+  return a.blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
+}
 
-template <bool WHT>
+constexpr int kBlocksThreads = 256;
+constexpr int kPlainBlocks = kBlocksThreads / 4;
+
+// Four lanes per block, chunks sub, sub + 4, sub + 8, sub + 12 of it each: the
+// four loads are in flight together, every load and store of the four lanes
+// covers whole sectors, and the amax takes two shuffles and the scale and its
+// reciprocal are formed once per 32 elements of a thread.
 __global__ void __launch_bounds__(kBlocksThreads) quant_blocks_kernel(const BlocksArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  const int group = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * (kUnroll * kGroups) + group;
-  uint4 d[kUnroll];
-  int64_t off[kUnroll];  // element offset of this lane's chunk, -1 past the data
+  const int sub = threadIdx.x & 3;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kPlainBlocks + (threadIdx.x >> 2);
+  const int64_t row = block_row(a, i), b = i - row * a.blocks;
+  const int left = i < a.total ? static_cast<int>(min(static_cast<int64_t>(128), a.K - b * 128)) - 8 * sub : 0;
+  const int64_t off = row * a.K + b * 128 + 8 * sub;
+  uint4 d[4];
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
-    const int64_t i = first + u * kGroups;
-    // i / blocks: exact while i * blocks < 2^64
-    const int64_t row = a.blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
-    const int64_t k = (i - row * a.blocks) * 128 + 8 * sub;
-    off[u] = i < a.total && k < a.K ? row * a.K + k : -1;
-    d[u] = off[u] >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.X + off[u])) : make_uint4(0, 0, 0, 0);
-  }
+  for (int u = 0; u < 4; ++u)
+    d[u] = 32 * u < left ? __ldg(reinterpret_cast<const uint4*>(a.X + off + 32 * u)) : make_uint4(0, 0, 0, 0);
+  float m = fmaxf(fmaxf(absmax_bf16x8(d[0]), absmax_bf16x8(d[1])), fmaxf(absmax_bf16x8(d[2]), absmax_bf16x8(d[3])));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const float s = row_global<1>(m);
+  const Divisor dv = make_divisor(s);
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < 4; ++u) {
     float v[8];
     unpack_bf16x8(d[u], v);
-    if (WHT) wht64_chunk(v, threadIdx.x & 31);
-    const float s = block_scale16(v);
-    const uint2 w = e4m3_codes8(v, make_divisor(s));
-    if (off[u] >= 0) {
-      *reinterpret_cast<uint2*>(a.codes + off[u]) = w;
-      if (sub == 0) {
-        const int64_t i = first + u * kGroups;
-        const int64_t row = a.blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
-        a.scales[(i - row * a.blocks) * a.rows + row] = s;
-      }
-    }
+    const uint2 w = e4m3_codes8(v, dv);
+    if (32 * u < left) *reinterpret_cast<uint2*>(a.codes + off + 32 * u) = w;
+  }
+  if (sub == 0 && i < a.total) a.scales[b * a.rows + row] = s;
+}
+
+// Rotated, few blocks: 16 lanes per block, the rotation over 8 of them.
+constexpr int kSpreadBlocks = kBlocksThreads / 16;
+
+__global__ void __launch_bounds__(kBlocksThreads) quant_rotated_spread_kernel(const BlocksArgs a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int sub = threadIdx.x & 15;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kSpreadBlocks + (threadIdx.x >> 4);
+  const int64_t row = block_row(a, i), b = i - row * a.blocks;
+  const int64_t k = b * 128 + 8 * sub;
+  const bool in = i < a.total && k < a.K;
+  float v[8];
+  unpack_bf16x8(in ? __ldg(reinterpret_cast<const uint4*>(a.X + row * a.K + k)) : make_uint4(0, 0, 0, 0), v);
+  wht64_chunk(v, threadIdx.x & 31);
+  const float s = block_scale16(v);
+  const uint2 w = e4m3_codes8(v, make_divisor(s));
+  if (in) {
+    *reinterpret_cast<uint2*>(a.codes + row * a.K + k) = w;
+    if (sub == 0) a.scales[b * a.rows + row] = s;
   }
 }
 
@@ -213,21 +229,13 @@ __global__ void __launch_bounds__(kWeightThreads, 4)
 // ------------------------------------------------- rotated blocks, many rows --
 // Rotations of plain bf16 input (weights, activations without a norm): a
 // thread transforms one whole 64-element block in its registers, so nothing
-// is exchanged between lanes (with the block over 8 lanes, 24 shuffles per 8
-// elements bound the kernel: 37888 x 3584 in 131 us).  A CTA takes 128 units of 128
-// elements at a time, the rows of a 128 x 128 weight block or 128 consecutive
-// 1 x 128 activation blocks; they come into shared memory by asynchronous
-// copies, one tile ahead, and lanes 2 i and 2 i + 1 read the halves of a unit.
-// 16-byte group c of unit u lies at group (c & 8) + ((c ^ u ^ c / 2 & 4) & 7),
-// which puts the eight lanes of each read phase on different banks.
+// is exchanged between lanes.  A CTA takes 128 rows x 128 columns at a time,
+// as two TMA boxes of 128 rows x 64 columns (128-byte swizzle), one tile
+// ahead; thread t has row t % 128 of box t / 128, so a quarter warp's 16-byte
+// reads fall on eight different swizzled positions.
 constexpr int kRotThreads = 256;
-constexpr int kRotUnits = kRotThreads / 2;
-constexpr int kRotTileBytes = kRotUnits * 256;
-constexpr int kRotSmem = 2 * kRotTileBytes;
-
-__device__ __forceinline__ uint32_t rot_offset(int unit, int c) {
-  return static_cast<uint32_t>(unit * 256 + ((c & 8) + ((c ^ unit ^ ((c >> 1) & 4)) & 7)) * 16);
-}
+constexpr int kRotBoxBytes = 128 * 128;
+constexpr int kRotSmem = 2 * 2 * kRotBoxBytes + 1024;
 
 // Unnormalised WHT of 64 values (8 times the normalised one), stages in the
 // sequential order, each sum and difference rounded once; the packed stages
@@ -250,62 +258,57 @@ __device__ __forceinline__ void wht64_thread(float2 (&v)[32]) {
 }
 
 struct RotArgs {
-  const __nv_bfloat16* X;
   int64_t rows, K;
-  int64_t k_blocks;
-  int64_t tiles;
-  unsigned long long inv_blocks;  // floor(2^64 / k_blocks) + 1 (k_blocks > 1)
+  uint32_t k_blocks, tiles;
   uint8_t* codes;
   float* scales;
+  long long budget;
 };
 
-// Row and column of unit u of a tile, row < 0 past the data.
 template <bool WEIGHT>
-__device__ __forceinline__ void rot_unit(const RotArgs& a, int64_t tile, int u, int64_t& row, int64_t& col) {
-  if (WEIGHT) {
-    const int64_t nb = a.k_blocks == 1 ? tile : static_cast<int64_t>(__umul64hi(tile, a.inv_blocks));
-    row = nb * 128 + u;
-    col = (tile - nb * a.k_blocks) * 128;
-  } else {
-    const int64_t i = tile * kRotUnits + u;
-    row = a.k_blocks == 1 ? i : static_cast<int64_t>(__umul64hi(i, a.inv_blocks));
-    col = (i - row * a.k_blocks) * 128;
-  }
-  if (row >= a.rows) row = -1;
-}
-
-template <bool WEIGHT>
-__global__ void __launch_bounds__(kRotThreads, 2) quant_rotated_kernel(const RotArgs a) {
-  extern __shared__ __align__(128) uint8_t s_tiles[];
+__global__ void __launch_bounds__(kRotThreads, 2)
+    quant_rotated_kernel(const __grid_constant__ CUtensorMap map, const RotArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[2];
   __shared__ float s_max[kRotThreads / 32];
+  __shared__ float s_half[kRotThreads];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  if (threadIdx.x == 0) {
+    prefetch_tensormap(&map);
+    mbar_init(&full_bar[0], 1);
+    mbar_init(&full_bar[1], 1);
+    fence_mbarrier_init();
+  }
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const uint32_t base = smem_u32(s_tiles);
-  // 16 lanes copy a unit; what lies past the data is filled with zeros
-  auto copy = [&](int64_t tile, int buf) {
-    if (tile < a.tiles) {
-      const int c = threadIdx.x & 15;
-#pragma unroll
-      for (int u = threadIdx.x >> 4; u < kRotUnits; u += kRotThreads / 16) {
-        int64_t row, col;
-        rot_unit<WEIGHT>(a, tile, u, row, col);
-        const bool in = row >= 0 && col + 8 * c < a.K;
-        cp_async16(base + buf * kRotTileBytes + rot_offset(u, c), in ? a.X + row * a.K + col + 8 * c : a.X, in);
-      }
+  auto load = [&](uint32_t tile, int buf) {
+    if (threadIdx.x == 0 && tile < a.tiles) {
+      const int row = static_cast<int>(tile / a.k_blocks * 128), col = static_cast<int>(tile % a.k_blocks * 128);
+      mbar_arrive_expect_tx(&full_bar[buf], 2 * kRotBoxBytes);
+      tma_load_2d(smem + 2 * buf * kRotBoxBytes, &map, &full_bar[buf], col, row);
+      tma_load_2d(smem + (2 * buf + 1) * kRotBoxBytes, &map, &full_bar[buf], col + 64, row);
     }
-    cp_async_commit();
   };
-  const int unit = threadIdx.x >> 1, half = threadIdx.x & 1;
-  copy(blockIdx.x, 0);
+  const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
+  load(blockIdx.x, 0);
   int buf = 0;
-  for (int64_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, buf ^= 1) {
-    copy(tile + gridDim.x, buf ^ 1);
-    cp_async_wait<1>();
-    __syncthreads();
+  uint32_t phase = 0;
+  for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
+    load(tile + gridDim.x, buf ^ 1);  // its previous contents were read before the last barrier
+    // the whole CTA gives up or nobody, after its loads had the time to land
+    if (!__syncthreads_and(mbar_wait(&full_bar[buf], phase, a.budget))) {
+      if (threadIdx.x == 0) atomicOr(&g_vlaq_block128_status, kStatusTimeout);
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1ll << 21)) {
+      }
+      break;
+    }
+    const uint32_t at = smem_u32(smem) + (2 * buf + half) * kRotBoxBytes + r * 128;
     float2 v[32];
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      const uint4 q = ld_shared_v4(base + buf * kRotTileBytes + rot_offset(unit, 8 * half + c));
+      const uint4 q = ld_shared_v4(at + ((c ^ (r & 7)) << 4));
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -318,32 +321,35 @@ __global__ void __launch_bounds__(kRotThreads, 2) quant_rotated_kernel(const Rot
     // the transform's factor 1/8, exact here (sums of bf16 values are
     // multiples of 2^-133), goes into the amax and the divisor
     m = __fmul_rn(m, 0.125f);
-    if (WEIGHT)
+    if (WEIGHT) {
       m = block_amax(m, s_max);
-    else
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    } else {
+      s_half[threadIdx.x] = m;
+      __syncthreads();
+      m = fmaxf(m, s_half[threadIdx.x ^ 128]);
+    }
     const float s = row_global<1>(m);
     const Divisor dv = make_divisor(__fmul_rn(s, 8.0f));
-    int64_t row, col;
-    rot_unit<WEIGHT>(a, tile, unit, row, col);
-    const bool in = row >= 0 && col + 64 * half < a.K;
-    uint32_t w[16];
+    const uint32_t nb = tile / a.k_blocks, kb = tile - nb * a.k_blocks;
+    const int64_t row = static_cast<int64_t>(nb) * 128 + r, col = static_cast<int64_t>(kb) * 128 + 64 * half;
+    const bool in = row < a.rows && col < a.K;
+    uint4* dst = reinterpret_cast<uint4*>(a.codes + row * a.K + col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float t[8] = {v[4 * i].x,     v[4 * i].y,     v[4 * i + 1].x, v[4 * i + 1].y,
-                          v[4 * i + 2].x, v[4 * i + 2].y, v[4 * i + 3].x, v[4 * i + 3].y};
-      const uint2 q = e4m3_codes8(t, dv);
-      w[2 * i] = q.x;
-      w[2 * i + 1] = q.y;
+    for (int i = 0; i < 4; ++i) {
+      const float2* p = v + 8 * i;
+      const float t[16] = {p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y,
+                           p[4].x, p[4].y, p[5].x, p[5].y, p[6].x, p[6].y, p[7].x, p[7].y};
+      const uint2 lo = e4m3_codes8(t, dv), hi = e4m3_codes8(t + 8, dv);
+      if (in) dst[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
     }
-    if (in) {
-      uint4* dst = reinterpret_cast<uint4*>(a.codes + row * a.K + col + 64 * half);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-      if (!WEIGHT && half == 0) a.scales[(col >> 7) * a.rows + row] = s;
+    if (WEIGHT) {
+      if (threadIdx.x == 0) a.scales[tile] = s;
+    } else if (half == 0 && row < a.rows) {
+      a.scales[static_cast<int64_t>(kb) * a.rows + row] = s;
     }
-    if (WEIGHT && threadIdx.x == 0) a.scales[tile] = s;
-    __syncthreads();  // the buffer (and s_max) have been read
+    __syncthreads();  // the buffer, s_max and s_half have been read
+    if (buf) phase ^= 1u;
+    buf ^= 1;
   }
 }
 
@@ -511,17 +517,30 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   return launch_norm_shape<RESID, WHT, OUT, 256, 16>(a, s);
 }
 
-// Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64.
+// Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64
+// elements (more CTAs, shorter chains).  64 x 3584 (1792 blocks) takes 2.8 us
+// spread and 3.6 in threads, 512 x 3584 (14336) 3.7 both ways.
 constexpr int64_t kFewBlocks = 8192;
 
 template <bool WEIGHT>
-cudaError_t launch_rotated(const RotArgs& r, cudaStream_t s) {
+cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
+  CUtensorMap map;
+  if (!make_bf16_map(&map, X, static_cast<uint64_t>(K), static_cast<uint64_t>(rows), 128)) return cudaErrorInvalidValue;
+  RotArgs r;
+  r.rows = rows;
+  r.K = K;
+  const int64_t k_blocks = (K + 127) / 128, tiles = (rows + 127) / 128 * k_blocks;
+  if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  r.k_blocks = static_cast<uint32_t>(k_blocks);
+  r.tiles = static_cast<uint32_t>(tiles);
+  r.codes = codes;
+  r.scales = scales;
+  r.budget = kWaitBudgetCycles;
   const cudaError_t e = cudaFuncSetAttribute(quant_rotated_kernel<WEIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kRotSmem);
   if (e != cudaSuccess) return e;
-  const int64_t ctas = 2 * static_cast<int64_t>(device_sm_count());
-  return launch_pdl(quant_rotated_kernel<WEIGHT>, dim3(static_cast<unsigned int>(r.tiles < ctas ? r.tiles : ctas)),
-                    dim3(kRotThreads), kRotSmem, s, r);
+  const uint32_t ctas = 2 * static_cast<uint32_t>(device_sm_count());
+  return launch_pdl(quant_rotated_kernel<WEIGHT>, dim3(r.tiles < ctas ? r.tiles : ctas), dim3(kRotThreads), kRotSmem, s, map, r);
 }
 
 }  // namespace
@@ -541,39 +560,42 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
     return wht ? launch_norm<false, true, kOutFp8>(a, s) : launch_norm<false, false, kOutFp8>(a, s);
   }
   const int64_t blocks = (K + 127) / 128;
-  const unsigned long long inv = blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(blocks) + 1;
-  // Few rotated blocks finish sooner spread over 8 lanes each: see launch_rotated
-  if (wht && M * blocks > kFewBlocks) {
-    RotArgs r = {static_cast<const __nv_bfloat16*>(X), M, K, blocks, (M * blocks + kRotUnits - 1) / kRotUnits, inv,
-                 codes, s_x};
-    return launch_rotated<false>(r, s);
-  }
+  if (wht && M * blocks > kFewBlocks) return launch_rotated<false>(X, M, K, codes, s_x, s);
   BlocksArgs a;
   a.X = static_cast<const __nv_bfloat16*>(X);
   a.rows = M;
   a.K = K;
   a.blocks = blocks;
   a.total = M * blocks;
-  a.inv_blocks = inv;
+  a.inv_blocks = blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(blocks) + 1;
   a.codes = codes;
   a.scales = s_x;
-  const int64_t grid = (a.total + kUnroll * kGroups - 1) / (kUnroll * kGroups);
+  const int per_cta = wht ? kSpreadBlocks : kPlainBlocks;
+  const int64_t grid = (a.total + per_cta - 1) / per_cta;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return launch_pdl(wht ? quant_blocks_kernel<true> : quant_blocks_kernel<false>,
-                    dim3(static_cast<unsigned int>(grid)), dim3(kBlocksThreads), 0, s, a);
+  return launch_pdl(wht ? quant_rotated_spread_kernel : quant_blocks_kernel, dim3(static_cast<unsigned int>(grid)),
+                    dim3(kBlocksThreads), 0, s, a);
 }
 
 cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
                                           float* s_w, cudaStream_t s) {
-  const int64_t blocks = (K + 127) / 128, tiles = ((N + 127) / 128) * blocks;
-  if (flags & kFlagHadamard) {
-    const unsigned long long inv = blocks == 1 ? 0 : ~0ull / static_cast<unsigned long long>(blocks) + 1;
-    RotArgs r = {static_cast<const __nv_bfloat16*>(W), N, K, blocks, tiles, inv, codes, s_w};
-    return launch_rotated<true>(r, s);
-  }
+  if (flags & kFlagHadamard) return launch_rotated<true>(W, N, K, codes, s_w, s);
+  const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(quant_weight_block_kernel, dim3(static_cast<unsigned int>(tiles)), dim3(kWeightThreads), 0, s,
                     static_cast<const __nv_bfloat16*>(W), N, K, codes, s_w);
+}
+
+cudaError_t read_and_clear_block128_status(unsigned int* out, cudaStream_t s) {
+  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_block128_status, sizeof(unsigned int), 0,
+                                            cudaMemcpyDeviceToHost, s);
+  if (e != cudaSuccess) return e;
+  e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return e;
+  const unsigned int zero = 0;
+  e = cudaMemcpyToSymbolAsync(g_vlaq_block128_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
+  if (e != cudaSuccess) return e;
+  return cudaStreamSynchronize(s);
 }
 
 cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s) {

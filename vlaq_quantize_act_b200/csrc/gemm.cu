@@ -1730,19 +1730,30 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t r
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// bf16 output [rows, cols] for TMA tile stores: box 64 columns x 32 rows
-// (128-byte rows), 128-byte swizzle.  Needs a 16-byte aligned base and
-// cols % 8 == 0.
-bool make_out_map(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows) {
+namespace {
+bool bf16_tiles(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                CUtensorMapL2promotion promotion) {
   EncodeTiledFn enc = get_encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {cols * 2};
-  const cuuint32_t box[2] = {64, 32};
+  const cuuint32_t box[2] = {64, box_rows};
   const cuuint32_t estr[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, promotion,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
+// bf16 output [rows, cols] for TMA tile stores: box 64 columns x 32 rows
+// (128-byte rows), 128-byte swizzle.  Needs a 16-byte aligned base and
+// cols % 8 == 0.
+bool make_out_map(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows) {
+  return bf16_tiles(map, base, cols, rows, 32, CU_TENSOR_MAP_L2_PROMOTION_NONE);
+}
+
+bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows) {
+  return bf16_tiles(map, base, cols, rows, box_rows, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
 namespace {

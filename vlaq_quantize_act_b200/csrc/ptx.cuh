@@ -484,6 +484,19 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
   return out;
 }
 
+// Four fp32 -> four E4M3 bytes, a in the low byte.
+__device__ __forceinline__ uint32_t cvt_e4m3x4(float a, float b, float c, float d) {
+  uint32_t out;
+  asm(
+      "{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(out)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return out;
+}
+
 // One E4M3 byte -> fp32 (exact).
 __device__ __forceinline__ float e4m3_to_f32(uint32_t byte) {
   uint32_t h2;

@@ -73,6 +73,38 @@ __device__ __forceinline__ void quotients(const float* v, const Divisor& d, floa
   }
 }
 
+// -RN(v[i] / S): the steps of quotients() from the negated product, which
+// negate no operand (a packed operand takes an instruction to negate):
+// n = x (-y), e = n S + x, r = e (-y) + n.  v = -0 gives +0 and +0 gives -0.
+template <int N>
+__device__ __forceinline__ void negated_quotients(const float* v, const Divisor& d, float* q) {
+  static_assert(N % 2 == 0, "pairs");
+  const float2 ny = make_float2(-d.y, -d.y);
+  const float2 ss = make_float2(d.S, d.S);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const float2 x = make_float2(v[i], v[i + 1]);
+    const float2 n = __fmul2_rn(x, ny);
+    const float2 e = __ffma2_rn(n, ss, x);
+    const float2 r = __ffma2_rn(e, ny, n);
+    q[i] = r.x;
+    q[i + 1] = r.y;
+  }
+  if (__any_sync(0xffffffffu, d.slow)) {
+    if (d.slow) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) q[i] = (d.S == 0.0f) ? -0.0f : -__fdiv_rn(v[i], d.S);
+    }
+  }
+}
+
+// E4M3 codes of RN(v[i] / S) for 8 values, element 0 in the low byte.
+__device__ __forceinline__ uint2 e4m3_codes8(const float* v, const Divisor& d) {
+  float q[8];
+  negated_quotients<8>(v, d, q);
+  return make_uint2(cvt_e4m3x4(q[0], q[1], q[2], q[3]) ^ 0x80808080u, cvt_e4m3x4(q[4], q[5], q[6], q[7]) ^ 0x80808080u);
+}
+
 // The global scale of a row from its amax A >= 0: RN(A / 2688) (NVFP4),
 // RN(A / 448) (FP8) or RN(A / 127) (INT8), by the correction step against
 // the constant's correctly rounded reciprocal; rows whose amax is tiny

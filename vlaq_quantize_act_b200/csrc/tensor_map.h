@@ -14,5 +14,7 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64_t r
 // bf16 tensor [rows, cols] in tiles of 64 columns x 32 rows (128-byte rows),
 // 128-byte swizzle.  Needs a 16-byte aligned base and cols % 8 == 0.
 bool make_out_map(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows);
+// The same to read, in tiles of 64 columns x box_rows rows.
+bool make_bf16_map(CUtensorMap* map, const void* base, uint64_t cols, uint64_t rows, uint32_t box_rows);
 
 }  // namespace vlaq
