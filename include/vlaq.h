@@ -321,7 +321,7 @@ VLAQ_API vlaq_status vlaq_linear_fp8(const uint8_t* xq, const float* s_x,
  * Finite inputs only.
  *
  * RMSNorm in these entry points is the formula of VLAQ_F_RMSNORM with the
- * sum of squares over 256 lanes instead of 32: lane l owns the 8-element
+ * sum of squares over 256 lanes instead of 32: lane l owns the 16-element
  * chunks l, l + 256, ... in element order (fused multiply-add), an XOR
  * butterfly 16, 8, 4, 2, 1 joins each 32 adjacent lanes and a butterfly
  * 1, 2, 4 the eight groups.  A row's result depends on that row alone. */

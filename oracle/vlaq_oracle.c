@@ -406,18 +406,18 @@ void vo_decode_fp8(const uint8_t* codes, const float* s, int64_t rows,
  * of a weight (s [NB, KB]): s = max|y| / 448 over the block (fp32), code =
  * E4M3(y / s) (RNE, saturate), or 0 when s == 0.
  *
- * RMSNorm here sums squares over 256 lanes: lane l owns the 8-element chunks
+ * RMSNorm here sums squares over 256 lanes: lane l owns the 16-element chunks
  * l, l + 256, ... in element order with a fused multiply-add, an XOR
  * butterfly 16, 8, 4, 2, 1 joins each 32 adjacent lanes, a butterfly 1, 2, 4
  * the eight groups.
  */
 float vo_sumsq_tree256(const float* x, int64_t K) {
   float lane[256], group[8];
-  int64_t nchunk = K / 8;
+  int64_t nchunk = K / 16;
   for (int l = 0; l < 256; ++l) {
     float acc = 0.0f;
     for (int64_t c = l; c < nchunk; c += 256)
-      for (int e = 0; e < 8; ++e) acc = fmaf(x[8 * c + e], x[8 * c + e], acc);
+      for (int e = 0; e < 16; ++e) acc = fmaf(x[16 * c + e], x[16 * c + e], acc);
     lane[l] = acc;
   }
   for (int g = 0; g < 8; ++g) {

@@ -118,9 +118,9 @@ def test_sumsq_tree256_order():
         x = (rng.integers(1, 64, K) * 2.0 ** rng.integers(-6, 7, K)).astype(np.float32)
         lane = np.zeros(256, np.float32)
         sq = (x.astype(np.float64) ** 2).astype(np.float32)
-        for c in range(K // 8):
-            for e in range(8):
-                lane[c % 256] = np.float32(lane[c % 256] + sq[8 * c + e])
+        for c in range(K // 16):
+            for e in range(16):
+                lane[c % 256] = np.float32(lane[c % 256] + sq[16 * c + e])
         g = lane.reshape(8, 32)
         for w in (16, 8, 4, 2, 1):
             g = (g[:, :w] + g[:, w:2 * w]).astype(np.float32)

@@ -15,10 +15,10 @@
 //
 // Sums of squares use a fixed tree of 256 lanes, so a row's result does not
 // depend on how many rows the call has or on the CTA's thread count: lane l
-// owns the chunks l, l + 256, ... and adds them in element order with fused
-// multiply-adds; an XOR butterfly 16, 8, 4, 2, 1 joins each group of 32 lanes
-// and a butterfly 1, 2, 4 the eight groups.  A thread of a CTA with T < 256
-// threads carries 256 / T of these lanes.
+// owns the 16-element chunks l, l + 256, ... and adds them in element order
+// with fused multiply-adds; an XOR butterfly 16, 8, 4, 2, 1 joins each group of
+// 32 lanes and a butterfly 1, 2, 4 the eight groups.  A thread of a CTA with T
+// < 256 threads carries 256 / T of these lanes.
 #include <cuda_bf16.h>
 
 #include "internal.h"
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
 }
 
 // --------------------------------------------------- rows with a norm --
-// One CTA per row, the row in registers (CPT chunks of 8 per thread).
+// One CTA per row, the row in registers (CPT chunks of 16 per thread).
 //   RESID:  t = RMSNorm(y) (or y), t *= gate, c = h + alpha t, h' = bf16(c)
 //   else:   c = x
 //   then    v = RMSNorm(c) from the unrounded fp32 c (skipped when the call
@@ -376,12 +376,35 @@ struct NormArgs {
   float* scales;         // [blocks][rows]
   int64_t rows;
   int K;
+  bool wide;  // every bf16 buffer is 32-byte aligned
 };
+
+// 16 bf16 values (32 bytes), in one access where their buffer's alignment
+// allows it.  Plain, ordered accesses: outputs may overwrite inputs in place.
+__device__ __forceinline__ void load_chunk(const __nv_bfloat16* p, bool wide, uint4& a, uint4& b) {
+  if (wide) {
+    ld_global_v8(p, a, b);
+  } else {
+    a = reinterpret_cast<const uint4*>(p)[0];
+    b = reinterpret_cast<const uint4*>(p)[1];
+  }
+}
+
+__device__ __forceinline__ void store_chunk(__nv_bfloat16* p, bool wide, const float* v) {
+  const uint4 a = pack_bf16x8(v), b = pack_bf16x8(v + 8);
+  if (wide) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    st_global_v8(p, w);
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = a;
+    reinterpret_cast<uint4*>(p)[1] = b;
+  }
+}
 
 // Sum of squares of a row in the 256-lane tree.  v: the thread's chunks in
 // order (chunk i is chunk t + T i of the row, zeros past it).
 template <int T, int CPT>
-__device__ __forceinline__ float tree_sumsq(const float (&v)[CPT][8], float* s_part) {
+__device__ __forceinline__ float tree_sumsq(const float (&v)[CPT][16], float* s_part) {
   constexpr int L = kTreeLanes / T;  // tree lanes per thread
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -390,7 +413,7 @@ __device__ __forceinline__ float tree_sumsq(const float (&v)[CPT][8], float* s_p
 #pragma unroll
     for (int i = l; i < CPT; i += L)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc = __fmaf_rn(v[i][j], v[i][j], acc);
+      for (int j = 0; j < 16; ++j) acc = __fmaf_rn(v[i][j], v[i][j], acc);
 #pragma unroll
     for (int o = 16; o; o >>= 1) acc = __fadd_rn(acc, __shfl_xor_sync(0xffffffffu, acc, o));
     if (lane == 0) s_part[warp + (T / 32) * l] = acc;  // group of tree lanes 32 g .. 32 g + 31
@@ -406,71 +429,105 @@ __device__ __forceinline__ float rms_factor(float ss, int K, float eps) {
   return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(mean, eps)));
 }
 
-// v = (v r) gamma for the thread's chunks.
+// Chunks of 16 bf16 factors (norm gains, gate rows), loaded ahead of their use.
 template <int T, int CPT>
-__device__ __forceinline__ void apply_norm(float (&v)[CPT][8], float r, const __nv_bfloat16* gamma, int chunks) {
+struct Factors {
+  uint4 w[CPT][2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, int chunks, bool wide) {
 #pragma unroll
-  for (int i = 0; i < CPT; ++i) {
-    const int c = threadIdx.x + T * i;
-    if (c < chunks) {
-      float g[8];
-      unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(gamma) + c), g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(__fmul_rn(v[i][j], r), g[j]);
+    for (int i = 0; i < CPT; ++i) {
+      const int c = threadIdx.x + T * i;
+      w[i][0] = w[i][1] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) load_chunk(p + 16 * c, wide, w[i][0], w[i][1]);
     }
+  }
+};
+
+// v[j] *= g[j].
+__device__ __forceinline__ void mul_chunk(float* v, const uint4* w) {
+  float g[16];
+  unpack_bf16x8(w[0], g);
+  unpack_bf16x8(w[1], g + 8);
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    const float2 r = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(g[j], g[j + 1]));
+    v[j] = r.x;
+    v[j + 1] = r.y;
   }
 }
 
+__device__ __forceinline__ void scale_chunk(float* v, float s) {
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    const float2 r = __fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(s, s));
+    v[j] = r.x;
+    v[j + 1] = r.y;
+  }
+}
+
+// CTAs per SM that the register count is bounded for.  One chunk per thread:
+// 48 registers and 1280 threads for bf16 outputs (4580 x 3584: 22.7 us; 24.2 at
+// 60 registers), 64 and 1024 for FP8 ones, which spill at 48 (1024 x 3584: 10.6
+// against 10.9 us).  Two chunks: 80 and 768 (4000 x 8192: 50 us, 62 unbounded).
+constexpr int norm_min_ctas(int threads, int chunks, int out) {
+  return chunks == 1 ? (out == 0 ? 1280 : 1024) / threads : chunks == 2 ? 768 / threads : 1;
+}
+
 template <bool RESID, bool WHT, int OUT, int T, int CPT>
-__global__ void __launch_bounds__(T) norm_rows_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(T, norm_min_ctas(T, CPT, OUT)) norm_rows_kernel(const NormArgs a) {
   __shared__ float s_part[2][kTreeLanes / 32];
-  const int K = a.K, chunks = K >> 3;
+  const int K = a.K, chunks = K >> 4;
   const int lane = threadIdx.x & 31;
   griddep_wait();
   griddep_launch_dependents();
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
     // plain loads of h and y: the outputs may overwrite them in place
-    const uint4* h4 = reinterpret_cast<const uint4*>(a.h + row * K);
-    uint4 hw[CPT];
-    float v[CPT][8];
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    const __nv_bfloat16* h = a.h + row * K;
+    uint4 hw[CPT][2];
+    float v[CPT][16];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = threadIdx.x + T * i;
-      hw[i] = c < chunks ? h4[c] : make_uint4(0, 0, 0, 0);
+      hw[i][0] = hw[i][1] = zero;
+      if (c < chunks) load_chunk(h + 16 * c, a.wide, hw[i][0], hw[i][1]);
     }
     if (RESID) {
-      const uint4* y4 = reinterpret_cast<const uint4*>(a.y + row * K);
+      const __nv_bfloat16* y = a.y + row * K;
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         const int c = threadIdx.x + T * i;
-        unpack_bf16x8(c < chunks ? y4[c] : make_uint4(0, 0, 0, 0), v[i]);
+        uint4 y0 = zero, y1 = zero;
+        if (c < chunks) load_chunk(y + 16 * c, a.wide, y0, y1);
+        unpack_bf16x8(y0, v[i]);
+        unpack_bf16x8(y1, v[i] + 8);
       }
       if (a.gamma_post) {
-        const float ss = tree_sumsq<T, CPT>(v, s_part[0]);
-        apply_norm<T, CPT>(v, rms_factor(ss, K, a.eps), a.gamma_post, chunks);
-      }
-      if (a.gate) {
-        const uint4* g4 = reinterpret_cast<const uint4*>(a.gate + (row / a.gate_rows) * K);
+        Factors<T, CPT> g;
+        g.load(a.gamma_post, chunks, a.wide);
+        const float r = rms_factor(tree_sumsq<T, CPT>(v, s_part[0]), K, a.eps);
 #pragma unroll
         for (int i = 0; i < CPT; ++i) {
-          const int c = threadIdx.x + T * i;
-          if (c < chunks) {
-            float g[8];
-            unpack_bf16x8(__ldg(g4 + c), g);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = __fmul_rn(v[i][j], g[j]);
-          }
+          scale_chunk(v[i], r);
+          mul_chunk(v[i], g.w[i]);
         }
       }
-      uint4* o4 = reinterpret_cast<uint4*>(a.h_out + row * K);
+      if (a.gate) {
+        Factors<T, CPT> g;
+        g.load(a.gate + (row / a.gate_rows) * K, chunks, a.wide);
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) mul_chunk(v[i], g.w[i]);
+      }
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
         const int c = threadIdx.x + T * i;
-        float h[8];
-        unpack_bf16x8(hw[i], h);
+        float hv[16];
+        unpack_bf16x8(hw[i][0], hv);
+        unpack_bf16x8(hw[i][1], hv + 8);
+        // one at a time: a packed multiply and add would be joined to one rounding
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = __fadd_rn(h[j], __fmul_rn(v[i][j], a.alpha));
-        if (c < chunks) o4[c] = pack_bf16x8(v[i]);
+        for (int j = 0; j < 16; ++j) v[i][j] = __fadd_rn(hv[j], __fmul_rn(v[i][j], a.alpha));
+        if (c < chunks) store_chunk(a.h_out + row * K + 16 * c, a.wide, v[i]);
       }
       if (OUT == kOutBf16 && !a.x_out) {
         __syncthreads();  // the next row reuses s_part
@@ -478,28 +535,41 @@ __global__ void __launch_bounds__(T) norm_rows_kernel(const NormArgs a) {
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < CPT; ++i) unpack_bf16x8(hw[i], v[i]);
+      for (int i = 0; i < CPT; ++i) {
+        unpack_bf16x8(hw[i][0], v[i]);
+        unpack_bf16x8(hw[i][1], v[i] + 8);
+      }
     }
-    const float ss = tree_sumsq<T, CPT>(v, s_part[1]);
-    apply_norm<T, CPT>(v, rms_factor(ss, K, a.eps), a.gamma_pre, chunks);
+    Factors<T, CPT> g;
+    g.load(a.gamma_pre, chunks, a.wide);
+    const float r = rms_factor(tree_sumsq<T, CPT>(v, s_part[1]), K, a.eps);
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
       const int c = threadIdx.x + T * i;
+      scale_chunk(v[i], r);
+      mul_chunk(v[i], g.w[i]);
       if (OUT == kOutBf16) {
-        if (c < chunks) reinterpret_cast<uint4*>(a.x_out + row * K)[c] = pack_bf16x8(v[i]);
+        if (c < chunks) store_chunk(a.x_out + row * K + 16 * c, a.wide, v[i]);
       } else if ((c & ~31) < chunks) {  // warp-uniform
-        if (WHT) wht64_chunk(v[i], lane);
-        const float s = block_scale16(v[i]);
-        const uint2 w = e4m3_codes8(v[i], make_divisor(s));
+        if (WHT) wht64_lanes(v[i], lane);
+        // a 1 x 128 block is on 8 adjacent lanes
+        float m = fmaxf(absmax8(v[i]), absmax8(v[i] + 8));
+#pragma unroll
+        for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        const float s = row_global<1>(m);
+        const Divisor dv = make_divisor(s);
+        const uint2 lo = e4m3_codes8(v[i], dv), hi = e4m3_codes8(v[i] + 8, dv);
         if (c < chunks) {
-          *reinterpret_cast<uint2*>(a.codes + row * K + 8 * c) = w;
-          if ((c & 15) == 0) a.scales[static_cast<int64_t>(c >> 4) * a.rows + row] = s;
+          *reinterpret_cast<uint4*>(a.codes + row * K + 16 * c) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          if ((c & 7) == 0) a.scales[static_cast<int64_t>(c >> 3) * a.rows + row] = s;
         }
       }
     }
     __syncthreads();  // the next row reuses s_part
   }
 }
+
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 template <bool RESID, bool WHT, int OUT, int T, int CPT>
 cudaError_t launch_norm_shape(const NormArgs& a, cudaStream_t s) {
@@ -511,16 +581,18 @@ cudaError_t launch_norm_shape(const NormArgs& a, cudaStream_t s) {
 
 template <bool RESID, bool WHT, int OUT>
 cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
-  if (a.K <= 2048) return launch_norm_shape<RESID, WHT, OUT, 256, 1>(a, s);
-  if (a.K <= 4096) return launch_norm_shape<RESID, WHT, OUT, 256, 2>(a, s);
-  if (a.K <= 8192) return launch_norm_shape<RESID, WHT, OUT, 256, 4>(a, s);
-  return launch_norm_shape<RESID, WHT, OUT, 256, 16>(a, s);
+  if (a.K <= 1024) return launch_norm_shape<RESID, WHT, OUT, 64, 1>(a, s);
+  if (a.K <= 2048) return launch_norm_shape<RESID, WHT, OUT, 128, 1>(a, s);
+  if (a.K <= 4096) return launch_norm_shape<RESID, WHT, OUT, 256, 1>(a, s);
+  if (a.K <= 8192) return launch_norm_shape<RESID, WHT, OUT, 256, 2>(a, s);
+  return launch_norm_shape<RESID, WHT, OUT, 256, 8>(a, s);
 }
 
 // Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64
-// elements (more CTAs, shorter chains).  64 x 3584 (1792 blocks) takes 2.8 us
-// spread and 3.6 in threads, 512 x 3584 (14336) 3.7 both ways.
-constexpr int64_t kFewBlocks = 8192;
+// elements (more CTAs, shorter chains): 512 x 3584 (14336 blocks) takes 3.0 us
+// spread and 3.6 in threads, 256 x 18944 (37888) 6.6 both ways, 1024 x 18944
+// (151552) 21.7 and 15.9.
+constexpr int64_t kFewBlocks = 40960;
 
 template <bool WEIGHT>
 cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
@@ -557,6 +629,7 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
     a.scales = s_x;
     a.rows = M;
     a.K = static_cast<int>(K);
+    a.wide = aligned32(a.h) && aligned32(a.gamma_pre);
     return wht ? launch_norm<false, true, kOutFp8>(a, s) : launch_norm<false, false, kOutFp8>(a, s);
   }
   const int64_t blocks = (K + 127) / 128;
@@ -614,6 +687,8 @@ cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s) {
   a.scales = r.s_x;
   a.rows = r.M;
   a.K = static_cast<int>(r.K);
+  a.wide = aligned32(a.h) && aligned32(a.y) && aligned32(a.gamma_post) && aligned32(a.gate) && aligned32(a.gamma_pre) &&
+           aligned32(a.h_out) && aligned32(a.x_out);
   if (!r.codes) return launch_norm<true, false, kOutBf16>(a, s);
   return (r.flags & kFlagHadamard) ? launch_norm<true, true, kOutFp8>(a, s) : launch_norm<true, false, kOutFp8>(a, s);
 }

@@ -111,58 +111,6 @@ struct RowArgs {
   float g_static;       // calibrated global scale (kStatic)
 };
 
-// Normalised WHT of the 64-block spread over lanes 4 g .. 4 g + 3 (16 values
-// each, element 16 (lane % 4) + j): stages h = 1, 2, 4, 8 inside the lane,
-// h = 16, 32 across lanes (xor 1, 2), then x 1/8 (exact) -- the stages of the
-// sequential butterfly in the same order.  Executed by the whole warp.
-// Stages h >= 2 run two butterflies per packed fp32x2 instruction (each lane
-// rounded once, so the values are those of the scalar steps): a + b, and
-// a - b as fma(b, -1, a), a single rounding of the same exact difference
-// (signed zeros included).  Across lanes the new value is p + s v with s = -1
-// in the upper lane and +1 in the lower one, again one fused multiply-add.
-__device__ __forceinline__ void wht64_lanes(float* v, int lane) {
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const float a = v[i], b = v[i + 1];
-    v[i] = __fadd_rn(a, b);
-    v[i + 1] = __fsub_rn(a, b);
-  }
-  const float2 m1 = make_float2(-1.0f, -1.0f);
-#pragma unroll
-  for (int h = 2; h < 16; h <<= 1) {
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      if ((i & h) == 0) {
-        const float2 a = make_float2(v[i], v[i + 1]), b = make_float2(v[i + h], v[i + h + 1]);
-        const float2 sum = __fadd2_rn(a, b), dif = __ffma2_rn(b, m1, a);
-        v[i] = sum.x;
-        v[i + 1] = sum.y;
-        v[i + h] = dif.x;
-        v[i + h + 1] = dif.y;
-      }
-    }
-  }
-#pragma unroll
-  for (int x = 1; x < 4; x <<= 1) {
-    const float sg = (lane & x) != 0 ? -1.0f : 1.0f;
-    const float2 s2 = make_float2(sg, sg);
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float2 p = make_float2(__shfl_xor_sync(0xffffffffu, v[i], x), __shfl_xor_sync(0xffffffffu, v[i + 1], x));
-      const float2 r = __ffma2_rn(make_float2(v[i], v[i + 1]), s2, p);
-      v[i] = r.x;
-      v[i + 1] = r.y;
-    }
-  }
-  const float2 e8 = make_float2(0.125f, 0.125f);
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) {
-    const float2 r = __fmul2_rn(make_float2(v[i], v[i + 1]), e8);
-    v[i] = r.x;
-    v[i + 1] = r.y;
-  }
-}
-
 // y_k / a_k or y_k * a_k for the 16 channels of block q (smoothing).
 __device__ __forceinline__ void smooth_block(const RowArgs& a, int q, float* v) {
   const float4* s4 = reinterpret_cast<const float4*>(a.smooth) + 4 * q;
