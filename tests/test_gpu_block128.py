@@ -215,7 +215,7 @@ def _check_linear(M, N, K, residual, seed=31, rows=None):
 @pytest.mark.parametrize("M,N,K", [(1, 8, 16), (1, 128, 128), (1, 4608, 3584), (2, 136, 144), (16, 264, 1040),
                                    (17, 128, 2048), (32, 120, 256), (33, 1000, 400), (64, 512, 3584), (65, 136, 272),
                                    (128, 392, 1168), (129, 264, 3584), (8, 3584, 2064), (5, 8, 32), (300, 392, 1024),
-                                   (257, 3584, 512), (333, 1000, 1040)])
+                                   (257, 3584, 512), (333, 1000, 1040), (37, 96, 352), (64, 18952, 144)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_linear_equals_the_fp64_product(M, N, K, residual):
     _check_linear(M, N, K, residual)
@@ -224,11 +224,22 @@ def test_linear_equals_the_fp64_product(M, N, K, residual):
 # CTA pairs: one tile per pair, several per pair with an odd count, ragged
 # rows / columns / depth, and fewer blocks than pipeline stages
 @pytest.mark.parametrize("M,N,K", [(1024, 2560, 1024), (1000, 2600, 1040), (2048, 3328, 272), (700, 3336, 16),
-                                   (1030, 4616, 400), (2300, 4104, 128)])
+                                   (1030, 4616, 400), (2300, 4104, 128), (2300, 9224, 128), (2048, 8200, 272),
+                                   (4096, 9224, 16)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_linear_over_cta_pairs_equals_the_fp64_product(M, N, K, residual):
     rng = np.random.default_rng(M)
     rows = np.unique(np.concatenate([rng.choice(M, 60, replace=False), [0, M - 1]]))
+    _check_linear(M, N, K, residual, rows=rows)
+
+
+# two CTA pairs per tile, half of K each: whole and ragged tiles, an odd number
+# of blocks, a last block of 112 columns
+@pytest.mark.parametrize("M,N,K", [(1280, 1024, 6144), (1270, 1000, 6000), (1281, 1032, 5104)])
+@pytest.mark.parametrize("residual", [False, True])
+def test_linear_over_two_pairs_per_tile_equals_the_fp64_product(M, N, K, residual):
+    rng = np.random.default_rng(M)
+    rows = np.unique(np.concatenate([rng.choice(M, 60, replace=False), [0, 127, 128, 255, M - 1]]))
     _check_linear(M, N, K, residual, rows=rows)
 
 

@@ -10,13 +10,18 @@
 // accumulator buffer is read while the next block's MMAs fill another.
 //   gemm_block_pair_kernel  256 x 256 tiles over the two CTAs of a cluster
 //                           (paired MMA), token rows on the TMEM lanes: one
-//                           scale per thread and block; prefill shapes.
-//   gemm_block_cols_kernel  128 weight rows on the TMEM lanes and NT token
-//                           columns (16 .. 128): a decode step's tile is as
-//                           narrow as its tokens, and the tile reads each
-//                           weight once; K is split over the CTAs of a cluster,
-//                           whose sums meet in shared memory (no workspace,
-//                           fixed order); decode and small shapes.
+//                           scale per thread and block; or over two pairs
+//                           that take half of K each.
+//   gemm_block_rows_kernel  128 tokens x 128 weight rows per CTA, token rows on
+//                           the lanes, K split over the CTAs of a cluster when
+//                           the tiles are few; more than 64 tokens whose
+//                           256 x 256 tiles would leave SMs idle.
+//   gemm_block_cols_kernel  128 weight rows on the TMEM lanes and 16, 32 or 64
+//                           token columns: a decode step's tile is as narrow
+//                           as its tokens, and the tile reads each weight
+//                           once; K split like that.
+// The CTAs of a cluster add their sums over each other's shared memory, in the
+// order of K: no workspace and the same result every time.
 //
 // Every mbarrier wait is bounded (clock budget); a wait that runs out sets a
 // shared abort flag and the device status word, the roles drain their own
@@ -151,26 +156,58 @@ __device__ __forceinline__ void epilogue_sync(int threads) {
   asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 }
 
-// Y[m, n .. n + 3] = bf16(sum over the cluster's CTAs, in rank order, of the
-// four fp32 sums at shared address `at` + residual).
-__device__ __forceinline__ void store_summed4(const BlockArgs& a, uint32_t at, int ctas, int m, int n) {
-  float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int r = 0; r < ctas; ++r) {
-    const float4 v = ld_shared_cluster_f4(mapa_shared(at, r));
-    y[0] += v.x;
-    y[1] += v.y;
-    y[2] += v.z;
-    y[3] += v.w;
-  }
+// Y[m, n .. n + 3] = bf16(y + residual).
+__device__ __forceinline__ void store4(const BlockArgs& a, float4 y, int m, int n) {
   const size_t o = static_cast<size_t>(m) * a.N + n;
   if (a.residual) {
     const uint2 rv = *reinterpret_cast<const uint2*>(a.residual + o);
-    y[0] += __uint_as_float(rv.x << 16);
-    y[1] += __uint_as_float(rv.x & 0xFFFF0000u);
-    y[2] += __uint_as_float(rv.y << 16);
-    y[3] += __uint_as_float(rv.y & 0xFFFF0000u);
+    y.x += __uint_as_float(rv.x << 16);
+    y.y += __uint_as_float(rv.x & 0xFFFF0000u);
+    y.z += __uint_as_float(rv.y << 16);
+    y.w += __uint_as_float(rv.y & 0xFFFF0000u);
   }
-  *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y[0], y[1]), bf16x2(y[2], y[3]));
+  *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
+}
+
+// Y[m, n .. n + 3] = bf16(sum over the cluster's CTAs, in rank order, of the
+// four fp32 sums at shared address `at` + residual).
+__device__ __forceinline__ void store_summed4(const BlockArgs& a, uint32_t at, int ctas, int m, int n) {
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int r = 0; r < ctas; ++r) {
+    const float4 v = ld_shared_cluster_f4(mapa_shared(at, r));
+    y.x += v.x;
+    y.y += v.y;
+    y.z += v.z;
+    y.w += v.w;
+  }
+  store4(a, y, m, n);
+}
+
+// Sums of the rows kernel's clusters: rows of 128 fp32 columns, 16-byte
+// groups permuted by the row and their halves swapped in rows 8 .. 15 mod 16,
+// so that a half warp's 8-byte writes, one row per lane, fall on all banks.
+// (Written 8 bytes at a time here and in the pair kernel: 16-byte stores tie
+// the sums to groups of four registers, and the multiply-adds of the loop
+// before took longer: 480 -> 600 ns for a block of the pair kernel, 50 -> 52 us
+// for 512 x 3584 x 18944 in the rows kernel.)
+constexpr int kSumRowBytes = 128 * 4;
+__device__ __forceinline__ uint32_t sum_offset(int row, int group) {
+  return static_cast<uint32_t>(row * kSumRowBytes + ((group ^ (row & 7)) << 4));
+}
+template <int COLS>
+__device__ __forceinline__ void write_sums(uint32_t base, int row, const float (&acc)[COLS], int group0 = 0) {
+  const uint32_t swap = static_cast<uint32_t>(row & 8);
+#pragma unroll
+  for (int c = 0; c < COLS; c += 4) {
+    const uint32_t at = base + sum_offset(row, group0 + c / 4);
+    st_shared_f2(at + swap, acc[c], acc[c + 1]);
+    st_shared_f2(at + (swap ^ 8u), acc[c + 2], acc[c + 3]);
+  }
+}
+// Four columns of a row in the CTA with that base.
+__device__ __forceinline__ float4 read_sums(uint32_t base, int row, int group) {
+  const float4 v = ld_shared_cluster_f4(base + sum_offset(row, group));
+  return row & 8 ? make_float4(v.z, v.w, v.x, v.y) : v;
 }
 
 // ---------------------------------------------------------------------------
@@ -200,6 +237,13 @@ __device__ __forceinline__ void store_summed4(const BlockArgs& a, uint32_t at, i
 // buffers overlap.  Measured against this split: 16 epilogue warps of 64
 // columns 172 / 380 us (more instructions per product), MMAs of 128 columns
 // with a barrier for each half 170 / 399 us (twice the round trips).
+//
+// SPLIT: few tiles and a long K.  A cluster of two pairs has one tile, each pair
+// half of its blocks; then each CTA sends the sums of half of its columns to
+// the other pair's CTA of its rows and stores the other half.  512 x 3584 x
+// 18944 (28 tiles): 67 -> 43 us; the exchange and the start of the larger
+// cluster cost about 3 us (reads of the other CTA's sums one row per lane, not
+// side by side: 8 us).
 struct PairTile {
   static constexpr int BM = 256, BN = 256;
   static constexpr int STAGE_BYTES = 2 * kTileBytes;
@@ -213,10 +257,12 @@ struct PairTile {
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_WARPS * 2 * OUT_BYTES + 1024;
   // kind::f8f6f4, E4M3 x E4M3, fp32 accumulator, N = 256, M = 256
   static constexpr uint32_t IDESC = (1u << 4) | (uint32_t(BN >> 3) << 17) | (uint32_t(BM >> 4) << 24);
+  static_assert(128 * COLS * 4 <= STAGES * STAGE_BYTES, "half of a CTA's sums fit its stages");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairTile::THREADS, 1)
+template <bool SPLIT>
+__global__ void __launch_bounds__(PairTile::THREADS, 1)
 gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmY, const __grid_constant__ CUtensorMap tmR,
                        const BlockArgs a) {
@@ -232,9 +278,15 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_ctarank();
-  const int pair = static_cast<int>(blockIdx.x >> 1);
+  const uint32_t cta = cluster_ctarank();
+  const uint32_t rank = cta & 1u;  // in the pair
+  // SPLIT: a cluster of two pairs has one tile, pair `split` half of its blocks
+  const int split = SPLIT ? static_cast<int>(cta >> 1) : 0;
+  const int pair = static_cast<int>(blockIdx.x >> (SPLIT ? 2 : 1));
   const int pairs = static_cast<int>(gridDim.x >> 1);
+  const int units = SPLIT ? pair + 1 : a.units;
+  const int kb0 = SPLIT && split ? a.blocks >> 1 : 0;
+  const int kb1 = SPLIT && !split ? a.blocks >> 1 : a.blocks;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::STAGES; ++i) {
@@ -261,8 +313,12 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   cluster_sync();  // both CTAs' barriers are initialised before either CTA signals the other's
   tc_fence_after();
   const uint32_t tmem = s_tmem_base;
-  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&s_abort)), rank ^ 1u);
-  const uint32_t leader_full = mapa_shared(smem_u32(full_bar), 0u);
+  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&s_abort)), cta ^ 1u);
+  const uint32_t leader_full = mapa_shared(smem_u32(full_bar), cta & ~1u);
+  const int first = (pair / a.m_tiles) * C::BN + 128 * static_cast<int>(rank);  // weight row of the first tile
+  keep(kb0, kb1, first);                                                       // computed before the wait
+  if (warp == 2 && elect_one())
+    for (int b = kb0; b < min(kb1, kb0 + kPrefetchBlocks); ++b) tma_prefetch_2d(&tmW, b * kRowBytes, first);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -276,9 +332,9 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       int it = 0, stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = pair; u < a.units && ok; u += pairs) {
+      for (int u = pair; u < units && ok; u += pairs) {
         const int row0 = (is_x ? (u % a.m_tiles) * C::BM : (u / a.m_tiles) * C::BN) + 128 * static_cast<int>(rank);
-        for (int b = 0; b < a.blocks; ++b, ++it) {
+        for (int b = kb0; b < kb1; ++b, ++it) {
           if (it >= C::STAGES && !bounded_wait(&done_bar[stage], phase ^ 1u, a.budget, &s_abort, peer_abort)) {
             ok = false;
             break;
@@ -309,8 +365,8 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       int stage = 0;
       uint32_t phase = 0, buf = 0;
       bool ok = true;
-      for (int u = pair; u < a.units && ok; u += pairs) {
-        for (int b = 0; b < a.blocks; ++b) {
+      for (int u = pair; u < units && ok; u += pairs) {
+        for (int b = kb0; b < kb1; ++b) {
           if (!bounded_wait(&full_bar[stage], phase, a.budget, &s_abort, peer_abort)) {
             ok = false;
             break;
@@ -320,7 +376,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             mma_f8f6f4_pair(tmem + buf, xd + off + 2 * j, wd + off + 2 * j, C::IDESC, j > 0);
-          umma_commit_pair(&done_bar[stage], 0x3);
+          umma_commit_pair(&done_bar[stage], static_cast<uint16_t>(0x3u << cta));
           buf ^= C::BN;
           if (++stage == C::STAGES) {
             stage = 0;
@@ -328,7 +384,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
           }
         }
       }
-      umma_commit_pair(&drain_bar, 0x1);
+      umma_commit_pair(&drain_bar, static_cast<uint16_t>(0x1u << cta));
       const long long t0 = clock64();
       while (!mbar_try_wait(&drain_bar, 0) && clock64() - t0 < 4 * a.budget + 1000000) {
       }
@@ -353,11 +409,12 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     float* slots = &s_sx[0][threadIdx.x - 128];
     uint32_t phase = 0, buf = 0;
     bool ok = true;
-    for (int u = pair; u < a.units && ok; u += pairs) {
+    for (int u = pair; u < units && ok; u += pairs) {
       const int row0 = (u % a.m_tiles) * C::BM + 128 * static_cast<int>(rank) + 32 * q;
       const int col0 = (u / a.m_tiles) * C::BN + C::COLS * h;
       const bool live = row0 < a.M && col0 < a.N;  // warp-uniform
-      if (a.residual && lane == 0) {
+      const bool stores = !SPLIT || h == split;  // this warp's columns are this CTA's to store
+      if (a.residual && stores && lane == 0) {
         // the residual lands in the staging buffer while the blocks are summed;
         // the previous tile's stores have read it by then
         bulk_wait_group_read0();
@@ -365,15 +422,15 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
         tma_load_2d(out + C::OUT_BYTES, &tmR, &res_bar[warp - 4], col0 + 64, row0);
       }
-      loading = a.residual != nullptr;
+      loading = a.residual && stores;
       // rows and columns past the output use the last ones' scales and are not stored
       ScaleStream<32 * C::EPI_WARPS> scales;
-      scales.start(a.sx + min(row0 + lane, a.M - 1), a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks,
-                   a.blocks, slots, a.M, lane);
+      scales.start(a.sx + static_cast<int64_t>(kb0) * a.M + min(row0 + lane, a.M - 1),
+                   a.sw + static_cast<int64_t>(min(col0, a.N - 1) >> 7) * a.blocks + kb0, kb1 - kb0, slots, a.M, lane);
       float acc[C::COLS];
 #pragma unroll
       for (int j = 0; j < C::COLS; ++j) acc[j] = 0.0f;
-      for (int b = 0; b < a.blocks; ++b) {
+      for (int b = 0; b < kb1 - kb0; ++b) {
         const float sc = scales.next(b, a.M, lane);
         if (!warp_wait(&done_bar[stage], phase, a.budget, &s_abort, peer_abort)) {
           ok = false;
@@ -392,6 +449,29 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         if (++stage == C::STAGES) {
           stage = 0;
           phase ^= 1u;
+        }
+      }
+      if (SPLIT) {
+        // Each CTA stores half of its rows' columns: the other half's sums go
+        // through the stages (all loads have landed and all MMAs have read
+        // them: the last block is done) to the CTA of the other pair.
+        // Two columns of all lanes side by side, which is how they are read.
+        const uint32_t sums = smem_u32(smem) + q * (32 * C::COLS * 4) + lane * 8;
+        if (ok && !stores) {
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 2) st_shared_f2(sums + c * 128, acc[c], acc[c + 1]);
+        }
+        __syncwarp();
+        cluster_sync();
+        if (!stores) break;
+        if (ok) {
+          const uint32_t other = mapa_shared(sums, cta ^ 2u);
+#pragma unroll
+          for (int c = 0; c < C::COLS; c += 2) {
+            const float2 v = ld_shared_cluster_f2(other + c * 128);
+            acc[c] += v.x;
+            acc[c + 1] += v.y;
+          }
         }
       }
       if (!ok) break;
@@ -438,10 +518,11 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     if (lane == 0) bulk_wait_group0();
   }
 
-  // Neither CTA leaves (or frees its TMEM) while the other may still signal
-  // it or the paired MMAs may still touch its shared memory or TMEM.
+  // No CTA leaves (or frees its TMEM) while another may still signal it, read
+  // its sums, or the paired MMAs may still touch its shared memory or TMEM.
   tc_fence_before();
   __syncwarp();
+  if (SPLIT && warp < 4) cluster_sync_relaxed();  // (the epilogue warps' exchange of sums)
   cluster_sync();
   if (warp == 1) {
     tc_fence_after();
@@ -475,12 +556,6 @@ struct RowsTile {
   static_assert(BUFS * BN <= kTmemColumns, "TMEM budget");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
-
-// Column group (16 bytes) c of row r of the cluster's sums: the groups of a
-// row are rotated by the row, so that the 32 rows of a warp fall on all banks.
-__device__ __forceinline__ uint32_t sums_offset(int r, int c) {
-  return static_cast<uint32_t>((r * (RowsTile::BN / 4) + (c ^ (r & 31))) * 16);
-}
 
 __global__ void __launch_bounds__(RowsTile::THREADS, 1)
 gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -664,10 +739,7 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       if (!ok) break;
       if (splits > 1) {
         // the ring is idle: every block of this CTA's range has been consumed
-#pragma unroll
-        for (int c = 0; c < C::COLS; c += 4)
-          st_shared_v4(smem_u32(smem) + sums_offset(32 * q + lane, (C::COLS * h + c) / 4), __float_as_uint(acc[c]),
-                       __float_as_uint(acc[c + 1]), __float_as_uint(acc[c + 2]), __float_as_uint(acc[c + 3]));
+        write_sums(smem_u32(smem), 32 * q + lane, acc, C::COLS * h / 4);
       } else {
         if (a.residual) {
           if (!warp_wait(&res_bar[warp - 4], res_phase, a.budget, &s_abort, 0)) break;
@@ -720,7 +792,15 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < rows * (C::BN / 4); i += splits * C::THREADS) {
       const int j = i / (C::BN / 4), c = i % (C::BN / 4), n = n0 + 4 * c;
       if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
-      store_summed4(a, sums + sums_offset(j, c), splits, m0 + j, n);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int r = 0; r < splits; ++r) {
+        const float4 v = read_sums(mapa_shared(sums, r), j, c);
+        y.x += v.x;
+        y.y += v.y;
+        y.z += v.z;
+        y.w += v.w;
+      }
+      store4(a, y, m0 + j, n);
     }
     __syncwarp();
     cluster_sync_relaxed();  // no CTA leaves while another reads its sums
@@ -952,15 +1032,19 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 #pragma unroll
         for (int j = 0; j < NT; ++j) sums[j * C::BN + 32 * q + lane] = acc[j];
       } else if (n < a.N) {
+        if (a.residual) {
+          // all of them on the way before the first is used (rows past the
+          // last token read the last one's): one at a time, 37 x 96 x 352 took
+          // 11.2 us
+          __nv_bfloat16 r[NT];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if (j < a.M) {
-            const size_t o = static_cast<size_t>(j) * a.N + n;
-            float y = acc[j];
-            if (a.residual) y += __bfloat162float(a.residual[o]);
-            a.Y[o] = __float2bfloat16_rn(y);
-          }
+          for (int j = 0; j < NT; ++j) r[j] = a.residual[static_cast<size_t>(min(j, a.M - 1)) * a.N + n];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[j] += __bfloat162float(r[j]);
         }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          if (j < a.M) a.Y[static_cast<size_t>(j) * a.N + n] = __float2bfloat16_rn(acc[j]);
       }
     }
   }
@@ -1042,9 +1126,10 @@ int clusters_resident(K kern, int size, int threads, int smem, std::atomic<int> 
   return n;
 }
 
-int pair_clusters() {
-  static std::atomic<int> cache[kMaxDevices];
-  const int n = clusters_resident(gemm_block_pair_kernel, 2, PairTile::THREADS, PairTile::SMEM_BYTES, cache);
+int pair_clusters(bool split) {
+  static std::atomic<int> cache[2][kMaxDevices];
+  auto kern = split ? gemm_block_pair_kernel<true> : gemm_block_pair_kernel<false>;
+  const int n = clusters_resident(kern, split ? 4 : 2, PairTile::THREADS, PairTile::SMEM_BYTES, cache[split]);
   return n > 0 ? n : 1;
 }
 
@@ -1060,6 +1145,8 @@ int cols_clusters(int splits) {
   static std::atomic<int> cache[kMaxSplits + 1][kMaxDevices];
   return clusters_resident(gemm_block_cols_kernel<NT>, splits, C::THREADS, C::SMEM_BYTES, cache[splits]);
 }
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // CTAs that share a tile: as many as keep every cluster resident at once, at
 // least two blocks of K each.
@@ -1083,7 +1170,7 @@ cudaError_t launch_tiles(Kernel kern, int threads, int smem, int units, int spli
                             args..., splits);
 }
 
-cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t s) {
+cudaError_t run_block_pair(const BlockLinear& l, bool split, long long budget, cudaStream_t s) {
   using C = PairTile;
   CUtensorMap tx, tw, ty, tr;
   const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
@@ -1091,16 +1178,17 @@ cudaError_t run_block_pair(const BlockLinear& l, long long budget, cudaStream_t 
   tr = ty;  // not read without a residual
   if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
   const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
-  const cudaError_t e =
-      cudaFuncSetAttribute(gemm_block_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  auto kern = split ? gemm_block_pair_kernel<true> : gemm_block_pair_kernel<false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int resident = pair_clusters();
-  const int pairs = a.units < resident ? a.units : resident;
-  return launch_pdl(gemm_block_pair_kernel, dim3(static_cast<unsigned int>(2 * pairs)), dim3(C::THREADS),
-                    C::SMEM_BYTES, s, tx, tw, ty, tr, a);
+  const int resident = pair_clusters(false);
+  const int clusters = split || a.units < resident ? a.units : resident;
+  const int ctas = split ? 4 : 2;
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned int>(ctas * clusters)), dim3(C::THREADS), ctas,
+                            C::SMEM_BYTES, s, tx, tw, ty, tr, a);
 }
 
-cudaError_t run_block_rows(const BlockLinear& l, long long budget, cudaStream_t s) {
+cudaError_t run_block_rows(const BlockLinear& l, int splits, long long budget, cudaStream_t s) {
   using C = RowsTile;
   CUtensorMap tx, tw, ty, tr;
   const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
@@ -1108,8 +1196,7 @@ cudaError_t run_block_rows(const BlockLinear& l, long long budget, cudaStream_t 
   tr = ty;  // not read without a residual
   if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
   const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
-  return launch_tiles(gemm_block_rows_kernel, C::THREADS, C::SMEM_BYTES, a.units,
-                      choose_splits(a.units, a.blocks, rows_clusters), s, tx, tw, ty, tr, a);
+  return launch_tiles(gemm_block_rows_kernel, C::THREADS, C::SMEM_BYTES, a.units, splits, s, tx, tw, ty, tr, a);
 }
 
 template <int NT>
@@ -1124,13 +1211,24 @@ cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t 
 
 }  // namespace
 
+// More than 64 tokens: the plan with the least estimated time, in ns of a cold
+// call: a start, and for every wave of tiles the blocks of K in turn.
+// (pair / pair, K in two / tiles of 128, us: 512 x 3584 x 3584 16.4 / 14.9 /
+// 12.3; 1024 x 3584 x 3584 17.4 / 29.3 / 21.5; 512 x 3584 x 18944 67 / 43 / 50;
+// 256 x 3584 x 18944 64 / 40 / 28; 1024 x 3584 x 18944 75 / 95 / 107.)
 cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s) {
   if (l.M <= 16) return run_block_cols<16>(l, budget, s);
   if (l.M <= 32) return run_block_cols<32>(l, budget, s);
   if (l.M <= 64) return run_block_cols<64>(l, budget, s);
-  const int64_t pair_units = ((l.M + 255) / 256) * ((l.N + 255) / 256);
-  if (pair_units * 2 > device_sm_count() / 2) return run_block_pair(l, budget, s);
-  return run_block_rows(l, budget, s);
+  const int64_t blocks = (l.K + 127) / 128;
+  const int64_t units = ceil_div(l.M, 256) * ceil_div(l.N, 256), tiles = ceil_div(l.M, 128) * ceil_div(l.N, 128);
+  const int64_t pair = 3500 + ceil_div(units, pair_clusters(false)) * (500 + 445 * blocks);
+  const int64_t halves = ceil_div(units, pair_clusters(true)) * (8000 + 235 * blocks);
+  const int splits = choose_splits(tiles, blocks, rows_clusters);
+  const int64_t rows = splits > 1 ? 4500 + 360 * ceil_div(blocks, splits)
+                                  : 3000 + ceil_div(tiles, device_sm_count()) * (300 + 360 * blocks);
+  if (rows <= pair && rows <= halves) return run_block_rows(l, splits, budget, s);
+  return run_block_pair(l, blocks > 1 && halves < pair, budget, s);
 }
 
 cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s) {
