@@ -6,12 +6,16 @@
 //   weight), code = E4M3_rne_sat(v / s), 0 where s = 0; the arithmetic of the
 //   per-row FP8 quantizer in smaller scopes.
 //
-// Rows are split into 8-element chunks (16 bytes of bf16), chunk c on thread
-// c % T of a CTA of T threads, so 16 adjacent lanes hold one 1 x 128 block
-// and 8 adjacent lanes one 64-element Hadamard block; the block's amax is
-// four shuffles, and a warp reads 512 contiguous bytes per load.  All kernels
-// are bound by HBM for many rows (2 or 4 bytes in, 1 to 4 out per element)
-// and by the launch and one memory round trip for one row.
+// Layouts, each chosen so that a thread's loads are in flight together and a
+// block's amax needs few exchanges:
+//   quant_blocks_kernel          4 lanes per 1 x 128 block, 32 elements each
+//   quant_rotated_spread_kernel  16 lanes per block, 8 elements each (few blocks)
+//   quant_rotated_kernel         one 64-element rotation per thread, tiles by TMA
+//   quant_weight_block_kernel    a CTA per 128 x 128 block, 64 elements a thread
+//   norm_rows_kernel             a CTA per row, 16-element chunks
+// All are bound by HBM for many rows (2 or 4 bytes in, 1 to 4 out per element;
+// the rotations by their instructions as well) and by the launch and one memory
+// round trip for one row.
 //
 // Sums of squares use a fixed tree of 256 lanes, so a row's result does not
 // depend on how many rows the call has or on the CTA's thread count: lane l
@@ -232,10 +236,14 @@ __global__ void __launch_bounds__(kWeightThreads, 4)
 // is exchanged between lanes.  A CTA takes 128 rows x 128 columns at a time,
 // as two TMA boxes of 128 rows x 64 columns (128-byte swizzle), one tile
 // ahead; thread t has row t % 128 of box t / 128, so a quarter warp's 16-byte
-// reads fall on eight different swizzled positions.
+// reads fall on eight different swizzled positions; the codes leave by one
+// TMA store per tile (stored by the threads, 64 bytes of a row each, 37888 x
+// 3584 took 95 us).  37888 x 3584: 78.7 us, 5.2 TB/s; 1024 x 18944: 14.7 us.  Two
+// CTAs per SM (the 64 values of a thread) alternate between memory and the
+// about 500 instructions of 64 elements, of which the rotation has 220.
 constexpr int kRotThreads = 256;
 constexpr int kRotBoxBytes = 128 * 128;
-constexpr int kRotSmem = 2 * 2 * kRotBoxBytes + 1024;
+constexpr int kRotSmem = (2 * 2 + 1) * kRotBoxBytes + 1024;
 
 // Unnormalised WHT of 64 values (8 times the normalised one), stages in the
 // sequential order, each sum and difference rounded once; the packed stages
@@ -258,16 +266,16 @@ __device__ __forceinline__ void wht64_thread(float2 (&v)[32]) {
 }
 
 struct RotArgs {
-  int64_t rows, K;
+  int64_t rows;
   uint32_t k_blocks, tiles;
-  uint8_t* codes;
   float* scales;
   long long budget;
 };
 
 template <bool WEIGHT>
 __global__ void __launch_bounds__(kRotThreads, 2)
-    quant_rotated_kernel(const __grid_constant__ CUtensorMap map, const RotArgs a) {
+    quant_rotated_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap out_map,
+                         const RotArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[2];
   __shared__ float s_max[kRotThreads / 32];
@@ -275,6 +283,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   if (threadIdx.x == 0) {
     prefetch_tensormap(&map);
+    prefetch_tensormap(&out_map);
     mbar_init(&full_bar[0], 1);
     mbar_init(&full_bar[1], 1);
     fence_mbarrier_init();
@@ -290,6 +299,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
       tma_load_2d(smem + (2 * buf + 1) * kRotBoxBytes, &map, &full_bar[buf], col + 64, row);
     }
   };
+  uint8_t* out = smem + 4 * kRotBoxBytes;  // codes of the tile, 128-byte swizzle
   const int r = threadIdx.x & 127, half = threadIdx.x >> 7;
   load(blockIdx.x, 0);
   int buf = 0;
@@ -321,6 +331,7 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     // the transform's factor 1/8, exact here (sums of bf16 values are
     // multiples of 2^-133), goes into the amax and the divisor
     m = __fmul_rn(m, 0.125f);
+    if (threadIdx.x == 0) bulk_wait_group_read0();  // the last tile's codes have left their buffer
     if (WEIGHT) {
       m = block_amax(m, s_max);
     } else {
@@ -331,26 +342,30 @@ __global__ void __launch_bounds__(kRotThreads, 2)
     const float s = row_global<1>(m);
     const Divisor dv = make_divisor(__fmul_rn(s, 8.0f));
     const uint32_t nb = tile / a.k_blocks, kb = tile - nb * a.k_blocks;
-    const int64_t row = static_cast<int64_t>(nb) * 128 + r, col = static_cast<int64_t>(kb) * 128 + 64 * half;
-    const bool in = row < a.rows && col < a.K;
-    uint4* dst = reinterpret_cast<uint4*>(a.codes + row * a.K + col);
+    const int64_t row = static_cast<int64_t>(nb) * 128 + r;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2* p = v + 8 * i;
       const float t[16] = {p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y,
                            p[4].x, p[4].y, p[5].x, p[5].y, p[6].x, p[6].y, p[7].x, p[7].y};
       const uint2 lo = e4m3_codes8(t, dv), hi = e4m3_codes8(t + 8, dv);
-      if (in) dst[i] = make_uint4(lo.x, lo.y, hi.x, hi.y);
+      st_shared_v4(smem_u32(out) + r * 128 + (((4 * half + i) ^ (r & 7)) << 4), lo.x, lo.y, hi.x, hi.y);
     }
     if (WEIGHT) {
       if (threadIdx.x == 0) a.scales[tile] = s;
     } else if (half == 0 && row < a.rows) {
       a.scales[static_cast<int64_t>(kb) * a.rows + row] = s;
     }
-    __syncthreads();  // the buffer, s_max and s_half have been read
+    fence_proxy_async_smem();
+    __syncthreads();  // the codes are written; the buffer, s_max and s_half have been read
+    if (threadIdx.x == 0) {
+      tma_store_2d(&out_map, out, static_cast<int>(kb * 128), static_cast<int>(nb * 128));  // clipped
+      bulk_commit_group();
+    }
     if (buf) phase ^= 1u;
     buf ^= 1;
   }
+  if (threadIdx.x == 0) bulk_wait_group0();
 }
 
 // --------------------------------------------------- rows with a norm --
@@ -589,30 +604,32 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
 }
 
 // Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64
-// elements (more CTAs, shorter chains): 512 x 3584 (14336 blocks) takes 3.0 us
-// spread and 3.6 in threads, 256 x 18944 (37888) 6.6 both ways, 1024 x 18944
-// (151552) 21.7 and 15.9.
-constexpr int64_t kFewBlocks = 40960;
+// elements (more CTAs, shorter chains; spread / in threads, us): 512 x 3584
+// (14336 blocks) 3.0 / 3.4, 1024 x 3584 (28672) 5.6 / 5.8, 8192 x 512 (32768) 6.1
+// / 6.0, 256 x 18944 (37888) 6.6 / 6.2, 1024 x 18944 (151552) 21.7 / 14.7.
+constexpr int64_t kFewBlocks = 30720;
 
 template <bool WEIGHT>
 cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
-  CUtensorMap map;
-  if (!make_bf16_map(&map, X, static_cast<uint64_t>(K), static_cast<uint64_t>(rows), 128)) return cudaErrorInvalidValue;
+  CUtensorMap map, out_map;
+  const uint64_t cols = static_cast<uint64_t>(K);
+  if (!make_bf16_map(&map, X, cols, static_cast<uint64_t>(rows), 128) ||
+      !make_map(&out_map, codes, cols, static_cast<uint64_t>(rows), cols, 128))
+    return cudaErrorInvalidValue;
   RotArgs r;
   r.rows = rows;
-  r.K = K;
   const int64_t k_blocks = (K + 127) / 128, tiles = (rows + 127) / 128 * k_blocks;
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   r.k_blocks = static_cast<uint32_t>(k_blocks);
   r.tiles = static_cast<uint32_t>(tiles);
-  r.codes = codes;
   r.scales = scales;
   r.budget = kWaitBudgetCycles;
   const cudaError_t e = cudaFuncSetAttribute(quant_rotated_kernel<WEIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kRotSmem);
   if (e != cudaSuccess) return e;
   const uint32_t ctas = 2 * static_cast<uint32_t>(device_sm_count());
-  return launch_pdl(quant_rotated_kernel<WEIGHT>, dim3(r.tiles < ctas ? r.tiles : ctas), dim3(kRotThreads), kRotSmem, s, map, r);
+  return launch_pdl(quant_rotated_kernel<WEIGHT>, dim3(r.tiles < ctas ? r.tiles : ctas), dim3(kRotThreads), kRotSmem, s,
+                    map, out_map, r);
 }
 
 }  // namespace
