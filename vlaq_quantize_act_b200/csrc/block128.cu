@@ -493,6 +493,9 @@ __global__ void __launch_bounds__(T, norm_min_ctas(T, CPT, OUT)) norm_rows_kerne
   __shared__ float s_part[2][kTreeLanes / 32];
   const int K = a.K, chunks = K >> 4;
   const int lane = threadIdx.x & 31;
+  // the gate row loaded before the post norm's sum where its registers are
+  // spare (1024 x 3584, FP8, a gate per row: 10.1 -> 9.6 us; 4580 rows bf16: 23.9 -> 25.0)
+  constexpr bool kGateAhead = OUT == kOutFp8 && CPT == 1;
   griddep_wait();
   griddep_launch_dependents();
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
@@ -517,6 +520,8 @@ __global__ void __launch_bounds__(T, norm_min_ctas(T, CPT, OUT)) norm_rows_kerne
         unpack_bf16x8(y0, v[i]);
         unpack_bf16x8(y1, v[i] + 8);
       }
+      Factors<T, CPT> gate;
+      if (kGateAhead && a.gate) gate.load(a.gate + (row / a.gate_rows) * K, chunks, a.wide);
       if (a.gamma_post) {
         Factors<T, CPT> g;
         g.load(a.gamma_post, chunks, a.wide);
@@ -528,10 +533,9 @@ __global__ void __launch_bounds__(T, norm_min_ctas(T, CPT, OUT)) norm_rows_kerne
         }
       }
       if (a.gate) {
-        Factors<T, CPT> g;
-        g.load(a.gate + (row / a.gate_rows) * K, chunks, a.wide);
+        if (!kGateAhead) gate.load(a.gate + (row / a.gate_rows) * K, chunks, a.wide);
 #pragma unroll
-        for (int i = 0; i < CPT; ++i) mul_chunk(v[i], g.w[i]);
+        for (int i = 0; i < CPT; ++i) mul_chunk(v[i], gate.w[i]);
       }
 #pragma unroll
       for (int i = 0; i < CPT; ++i) {
