@@ -56,7 +56,8 @@ def _act(X, gamma=None, flags=0):
 # one block; partial blocks; one row; more blocks than a CTA's round; the
 # limits of each row length's kernel; several rows per block of threads
 @pytest.mark.parametrize("M,K", [(1, 16), (3, 128), (5, 144), (1, 3584), (70, 336), (130, 1040), (4, 2048), (3, 2064),
-                                 (2, 4096), (3, 4112), (2, 8192), (2, 8208), (3, 18944), (1, 32768), (9500, 64)])
+                                 (2, 4096), (3, 4112), (2, 8192), (2, 8208), (2, 16384), (2, 16400), (3, 18944), (1, 32768),
+                                 (9500, 64), (31000, 64), (1700, 2368)])
 @pytest.mark.parametrize("flags", [0, RMS, HAD, RMS | HAD])
 def test_act_blocks_equal_the_oracle(M, K, flags):
     if flags & HAD and K % 64:
@@ -132,8 +133,8 @@ def _b(t):
     return None if t is None else bits(t)
 
 
-@pytest.mark.parametrize("M,K", [(1, 16), (3, 144), (7, 3584), (300, 336), (2, 2048), (5, 4112), (3, 8192), (2, 18944),
-                                 (1, 32768), (9500, 64)])
+@pytest.mark.parametrize("M,K", [(1, 16), (3, 144), (7, 3584), (300, 336), (2, 2048), (5, 4112), (3, 8192), (2, 8256),
+                                 (2, 16384), (2, 18944), (1, 32768), (9500, 64)])
 @pytest.mark.parametrize("post,gate,alpha", [(True, "none", 1.0), (False, "token", 0.5), (True, "vector", 0.22),
                                              (False, "none", -1.5), (True, "group", 1.0)])
 def test_residual_norm_equals_the_oracle(M, K, post, gate, alpha):
@@ -408,3 +409,111 @@ def test_weights_quantized_right_before_the_linear():
             m.vlaq_linear_fp8_block(xq, sx, wq, sw, None, Y2 if order else Y, M, N, K)
         torch.cuda.synchronize()
         assert torch.isfinite(Y.float()).all() and torch.equal(Y, Y2)
+
+
+# ------------------------------------------------------- buffers and offsets
+def _odd16(t):
+    """A copy that starts 16 bytes past a 256-byte boundary, with guard bytes
+    (0xFF) behind it, and the whole buffer."""
+    n = t.numel() * t.element_size()
+    buf = torch.full((n + 16 + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    view = buf[16:16 + n].view(t.dtype).view(t.shape)
+    view.copy_(t)
+    return view, buf
+
+
+def _guard_kept(view, buf, what):
+    n = view.numel() * view.element_size()
+    assert (buf[:16] == 0xFF).all() and (buf[16 + n:] == 0xFF).all(), f"{what}: written outside"
+
+
+@pytest.mark.parametrize("M,K", [(5, 272), (3, 3584), (33, 4160), (600, 7616)])
+def test_buffers_on_odd_16_bytes(M, K):
+    """Every buffer at 16 bytes past a 32-byte boundary gives the bytes of
+    aligned ones, and nothing before or behind an output is written."""
+    m = vq()
+    h, y, gp, g, gt = (None if t is None else t.cuda() for t in _norm_case(M, K, True, 2))
+    N = 136
+    W, R = si.projection_weight(K, N, 5).cuda(), si.residual(M, N, 5).cuda()
+    had = HAD if K % 64 == 0 else 0
+
+    def run(place):
+        P = {k: place(v) for k, v in dict(h=h, y=y, gp=gp, g=g, gt=gt, W=W, R=R).items()}
+        out = {}
+
+        def new(name, *shape, dtype):
+            out[name] = place(torch.zeros(*shape, dtype=dtype, device="cuda"))
+            return out[name][0]
+        v = {k: p[0] for k, p in P.items()}
+        u8, f32, b16 = torch.uint8, torch.float32, torch.bfloat16
+        kb, nb = -(-K // 128), -(-N // 128)
+        H, X = new("H", M, K, dtype=b16), new("X", M, K, dtype=b16)
+        m.vlaq_residual_norm(v["h"], v["y"], M, K, v["gp"], v["gt"], 2, 0.5, v["g"], 1e-6, H, X)
+        for f in (0, had):
+            H8, c, s = new(f"H8{f}", M, K, dtype=b16), new(f"c{f}", M, K, dtype=u8), new(f"s{f}", kb, M, dtype=f32)
+            m.vlaq_residual_norm_fp8_block(v["h"], v["y"], M, K, v["gp"], v["gt"], 2, 0.5, v["g"], 1e-6, f, H8, c, s)
+            c, s = new(f"ac{f}", M, K, dtype=u8), new(f"as{f}", kb, M, dtype=f32)
+            m.vlaq_quantize_act_fp8_block(v["y"], M, K, None, 1e-6, f, c, s)
+            cn, sn = new(f"nc{f}", M, K, dtype=u8), new(f"ns{f}", kb, M, dtype=f32)
+            m.vlaq_quantize_act_fp8_block(v["y"], M, K, v["g"], 1e-6, f | RMS, cn, sn)
+            cw, sw = new(f"wc{f}", N, K, dtype=u8), new(f"ws{f}", nb, kb, dtype=f32)
+            m.vlaq_quantize_weight_fp8_block(v["W"], N, K, f, cw, sw)
+            Y = new(f"Y{f}", M, N, dtype=b16)
+            m.vlaq_linear_fp8_block(c, s, cw, sw, v["R"], Y, M, N, K)
+        torch.cuda.synchronize()
+        m.vlaq_check()
+        return out
+
+    want, got = run(lambda t: (t.clone(), None)), run(_odd16)
+    for k in want:
+        assert torch.equal(want[k][0], got[k][0]), k
+        _guard_kept(*got[k], k)
+
+
+def test_offsets_past_32_bits():
+    """The last rows of tensors of more than 2^31 elements equal the same rows
+    in a call of their own."""
+    m = vq()
+    M, K = 66000, 32768
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(7)
+    X = torch.empty(M, K, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    g = si.norm_gain(K, 3).cuda()
+    rows = 130  # the last ones
+    codes, s = m.alloc_fp8_block(M, K)
+    for flags in (0, HAD, RMS):
+        m.vlaq_quantize_act_fp8_block(X, M, K, g, 1e-6, flags, codes, s)
+        c2, s2 = m.alloc_fp8_block(rows, K)
+        m.vlaq_quantize_act_fp8_block(X[M - rows:], rows, K, g, 1e-6, flags, c2, s2)
+        assert torch.equal(codes[M - rows:], c2) and torch.equal(s[:, M - rows:], s2), flags
+    for flags in (0, HAD):
+        cw, sw = m.alloc_fp8_block(M, K, weight=True)
+        m.vlaq_quantize_weight_fp8_block(X, M, K, flags, cw, sw)
+        n = M - M // 128 * 128 + 128  # whole blocks from the end
+        c2, s2 = m.alloc_fp8_block(n, K, weight=True)
+        m.vlaq_quantize_weight_fp8_block(X[M - n:], n, K, flags, c2, s2)
+        assert torch.equal(cw[M - n:], c2) and torch.equal(sw[-2:], s2), flags
+    del cw
+    H, Xo = torch.empty_like(X), torch.empty_like(X)
+    m.vlaq_residual_norm(X, X, M, K, g, X, 2, 0.5, g, 1e-6, H, Xo)
+    h2, x2 = torch.empty_like(X[:rows]), torch.empty_like(X[:rows])
+    m.vlaq_residual_norm(X[M - rows:], X[M - rows:], rows, K, g, X[(M - rows) // 2:], 2, 0.5, g, 1e-6, h2, x2)
+    assert torch.equal(H[M - rows:], h2) and torch.equal(Xo[M - rows:], x2)
+    del H, Xo, X, codes
+    # Y and the residual of more than 2^31 elements
+    N, k = 32776, 144
+    x = torch.empty(M, k, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    w = torch.empty(N, k, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    xq, sx = m.alloc_fp8_block(M, k)
+    wq, sw = m.alloc_fp8_block(N, k, weight=True)
+    m.vlaq_quantize_act_fp8_block(x, M, k, None, 1e-6, 0, xq, sx)
+    m.vlaq_quantize_weight_fp8_block(w, N, k, 0, wq, sw)
+    R = torch.empty(M, N, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)
+    last = R[M - 3:].cpu()
+    m.vlaq_linear_fp8_block(xq, sx, wq, sw, R, R, M, N, k)
+    torch.cuda.synchronize()
+    m.vlaq_check()
+    n = {a: b.cpu().numpy() for a, b in dict(xq=xq[M - 3:], sx=sx[:, M - 3:].contiguous(), wq=wq, sw=sw).items()}
+    dx, dw = oracle.decode_fp8_block(n["xq"], n["sx"]), oracle.decode_weight_fp8_block(n["wq"], n["sw"])
+    _check_gemm(R[M - 3:].float().cpu().numpy(), oracle.linear_f64(dx, dw, bits(last)), dx, dw, k,
+                residual_f64(last, np.arange(3)), "last rows")

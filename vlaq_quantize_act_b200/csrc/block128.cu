@@ -484,8 +484,10 @@ __device__ __forceinline__ void scale_chunk(float* v, float s) {
 // 48 registers and 1280 threads for bf16 outputs (4580 x 3584: 22.7 us; 24.2 at
 // 60 registers), 64 and 1024 for FP8 ones, which spill at 48 (1024 x 3584: 10.6
 // against 10.9 us).  Two chunks: 80 and 768 (4000 x 8192: 50 us, 62 unbounded).
+// Four: 128 and 512, some forms spill 40 words (1024 x 16384 bf16 34.8 us, 43.4
+// unbounded; 54 us with the eight chunks of the longest rows).
 constexpr int norm_min_ctas(int threads, int chunks, int out) {
-  return chunks == 1 ? (out == 0 ? 1280 : 1024) / threads : chunks == 2 ? 768 / threads : 1;
+  return chunks == 1 ? (out == 0 ? 1280 : 1024) / threads : chunks == 2 ? 768 / threads : chunks == 4 ? 2 : 1;
 }
 
 template <bool RESID, bool WHT, int OUT, int T, int CPT>
@@ -604,6 +606,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
   if (a.K <= 2048) return launch_norm_shape<RESID, WHT, OUT, 128, 1>(a, s);
   if (a.K <= 4096) return launch_norm_shape<RESID, WHT, OUT, 256, 1>(a, s);
   if (a.K <= 8192) return launch_norm_shape<RESID, WHT, OUT, 256, 2>(a, s);
+  if (a.K <= 16384) return launch_norm_shape<RESID, WHT, OUT, 256, 4>(a, s);
   return launch_norm_shape<RESID, WHT, OUT, 256, 8>(a, s);
 }
 
