@@ -216,7 +216,7 @@ def _check_linear(M, N, K, residual, seed=31, rows=None):
 @pytest.mark.parametrize("M,N,K", [(1, 8, 16), (1, 128, 128), (1, 4608, 3584), (2, 136, 144), (16, 264, 1040),
                                    (17, 128, 2048), (32, 120, 256), (33, 1000, 400), (64, 512, 3584), (65, 136, 272),
                                    (128, 392, 1168), (129, 264, 3584), (8, 3584, 2064), (5, 8, 32), (300, 392, 1024),
-                                   (257, 3584, 512), (333, 1000, 1040), (37, 96, 352), (64, 18952, 144)])
+                                   (257, 3584, 512), (333, 1000, 1040), (37, 96, 352), (64, 18952, 144), (40, 19000, 1488)])
 @pytest.mark.parametrize("residual", [False, True])
 def test_linear_equals_the_fp64_product(M, N, K, residual):
     _check_linear(M, N, K, residual)

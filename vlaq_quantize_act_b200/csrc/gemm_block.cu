@@ -540,6 +540,14 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 // Four accumulator buffers of 128 columns, block i in buffer i % 4; as in the
 // pair kernel the full barrier of block i also waits for the epilogue warps
 // that have read block i - 4.
+//
+// What bounds it: a block takes about 310 ns (600 clocks) in a long K, of which
+// shared memory takes 512: 32 KB in by TMA and 32 KB out to the MMA, whose own
+// time is 256.  512 x 3584 x 3584: 12.3 us (112 tiles), 128 x 3584 x 3584 8.4
+// (28 tiles of five CTAs, HBM and the first stage), 333 x 1000 x 2000 7.2.
+// Measured against it: epilogue warps in two sets that take alternate blocks,
+// 128 columns each, the same within 3%; four stages 12.5 us, prefetching
+// weights 6 or 12 blocks ahead 13.1.
 struct RowsTile {
   static constexpr int BM = 128, BN = 128;
   static constexpr int STAGE_BYTES = 2 * kTileBytes;
@@ -819,6 +827,10 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 // weights stream once.  Clusters, roles and barriers as in the kernel above,
 // with four epilogue warps; the token scales of CHUNK blocks at a time go
 // through shared memory, copied by the epilogue warps one chunk ahead.
+//
+// What bounds it: HBM for the weights, behind about 3 us of start, first round
+// trip and cluster sum.  8 x 3584 x 18944 14.4 us (4.7 TB/s), 4 x 37888 x 3584
+// 23.9 (5.7), 1 x 4608 x 3584 6.2.
 template <int NT>
 struct ColsTile {
   static constexpr int BN = 128;  // weight rows
@@ -1214,23 +1226,33 @@ cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t 
 
 }  // namespace
 
+// Up to 64 tokens: columns of 16, 32 or 64 tokens (in columns twice as wide 1 x
+// 4608 x 3584 takes 6.9 us instead of 6.2, 32 x 3584 x 18944 19.4 instead of 15.4).
+// Past 32, the tiles of 128 tokens start 0.7 us later but take less time for a
+// block, which pays from about 20 blocks in a row on (columns / rows, us: 33 x
+// 3584 x 3584, 7 blocks, 7.5 / 8.3; 48 x 18944 x 2048, 16, 12.4 / 13.0; 64 x 3584 x
+// 18944, 37, 19.6 / 18.0; 64 x 37888 x 3584, 56, 31 / 26).
+//
 // More than 64 tokens: the plan with the least estimated time, in ns of a cold
 // call: a start, and for every wave of tiles the blocks of K in turn.
 // (pair / pair, K in two / tiles of 128, us: 512 x 3584 x 3584 16.4 / 14.9 /
 // 12.3; 1024 x 3584 x 3584 17.4 / 29.3 / 21.5; 512 x 3584 x 18944 67 / 43 / 50;
 // 256 x 3584 x 18944 64 / 40 / 28; 1024 x 3584 x 18944 75 / 95 / 107.)  The
 // constants are fits to 110 shapes of 65 to 4580 tokens, widths to 37888 and
-// depths to 18944; the plan chosen took 2% longer than the best on average, 20%
+// depths to 18944; the plan chosen took 1.3% longer than the best on average, 19%
 // at most.
 cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s) {
   if (l.M <= 16) return run_block_cols<16>(l, budget, s);
   if (l.M <= 32) return run_block_cols<32>(l, budget, s);
-  if (l.M <= 64) return run_block_cols<64>(l, budget, s);
   const int64_t blocks = (l.K + 127) / 128;
   const int64_t units = ceil_div(l.M, 256) * ceil_div(l.N, 256), tiles = ceil_div(l.M, 128) * ceil_div(l.N, 128);
+  int splits = choose_splits(tiles, blocks, rows_clusters);
+  if (l.M <= 64) {
+    const int64_t in_a_row = ceil_div(tiles, splits > 1 ? tiles : device_sm_count()) * ceil_div(blocks, splits);
+    return in_a_row <= 20 ? run_block_cols<64>(l, budget, s) : run_block_rows(l, splits, budget, s);
+  }
   const int64_t pair = 2700 + ceil_div(units, pair_clusters(false)) * (1800 + 455 * blocks);
   const int64_t halves = ceil_div(units, pair_clusters(true)) * (8600 + 245 * blocks) - 1500;
-  int splits = choose_splits(tiles, blocks, rows_clusters);
   int64_t rows = 2600 + ceil_div(tiles, device_sm_count()) * (1000 + 338 * blocks);
   const int64_t rows_split = 5600 + 338 * ceil_div(blocks, splits);
   if (rows_split < rows && splits > 1)
