@@ -1160,16 +1160,23 @@ int cols_clusters(int splits) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// CTAs that share a tile: as many as keep every cluster resident at once, at
-// least two blocks of K each; no more than the longest range of blocks needs
-// (333 x 1000 x 2000, 16 blocks: 7.5 us by fours, 8.3 with five CTAs).
+// Time of a tile split over a cluster that does not depend on its depth (start,
+// first round trip, sum), in ns, and of a block of K: clusters of four start
+// fastest (333 x 1000 x 1040, by 1, 2, 3, 4 CTAs: 7.1, 7.7, 7.0, 6.7 us; 300 x 512
+// x 3584, by 4, 5, 6, 8: 7.1, 7.6, 7.4, 7.3).
+constexpr int64_t kBlockNs = 338;
+int64_t split_ns(int64_t blocks, int splits) {
+  return (splits < 4 ? 5850 : splits == 4 ? 5600 : 6500) + kBlockNs * ceil_div(blocks, splits);
+}
+
+// CTAs that share a tile: the fastest size that keeps every cluster resident at
+// once, with at least two blocks of K for each CTA; 1 where none does.
 template <typename Resident>
 int choose_splits(int64_t tiles, int64_t blocks, Resident resident) {
-  for (int splits = kMaxSplits; splits > 1; --splits)
-    if (blocks >= 2 * splits && tiles <= resident(splits) &&
-        (splits == 2 || ceil_div(blocks, splits - 1) > ceil_div(blocks, splits)))
-      return splits;
-  return 1;
+  int best = 1;
+  for (int splits = 2; splits <= kMaxSplits && blocks >= 2 * splits; ++splits)
+    if (tiles <= resident(splits) && (best == 1 || split_ns(blocks, splits) < split_ns(blocks, best))) best = splits;
+  return best;
 }
 
 // Tiles of one CTA each (grid capped at the SMs, which loop), or of a cluster.
@@ -1253,10 +1260,9 @@ cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cuda
   }
   const int64_t pair = 2700 + ceil_div(units, pair_clusters(false)) * (1800 + 455 * blocks);
   const int64_t halves = ceil_div(units, pair_clusters(true)) * (8600 + 245 * blocks) - 1500;
-  int64_t rows = 2600 + ceil_div(tiles, device_sm_count()) * (1000 + 338 * blocks);
-  const int64_t rows_split = 5600 + 338 * ceil_div(blocks, splits);
-  if (rows_split < rows && splits > 1)
-    rows = rows_split;
+  int64_t rows = 2600 + ceil_div(tiles, device_sm_count()) * (1000 + kBlockNs * blocks);
+  if (splits > 1 && split_ns(blocks, splits) < rows)
+    rows = split_ns(blocks, splits);
   else
     splits = 1;
   if (rows <= pair && rows <= halves) return run_block_rows(l, splits, budget, s);
