@@ -163,6 +163,11 @@ def test_residual_norm_equals_the_oracle(M, K, post, gate, alpha):
     m.vlaq_residual_norm(h2, y2, M, K, gpd, gtd, gate_rows, alpha, gd, 1e-6, h2, y2)
     _same(_bf16_bits(h2), ho, "h in place")
     _same(_bf16_bits(y2), xo, "x over y")
+    h2, y2 = hd.clone(), yd.clone()
+    m.vlaq_residual_norm(h2, y2, M, K, gpd, gtd, gate_rows, alpha, gd, 1e-6, y2, X.zero_())
+    _same(_bf16_bits(y2), ho, "h over y")
+    _same(_bf16_bits(X), xo, "x, h over y")
+    assert torch.equal(h2, hd)
 
 
 def test_residual_norm_of_zero_rows_is_finite():
@@ -517,3 +522,32 @@ def test_offsets_past_32_bits():
     dx, dw = oracle.decode_fp8_block(n["xq"], n["sx"]), oracle.decode_weight_fp8_block(n["wq"], n["sw"])
     _check_gemm(R[M - 3:].float().cpu().numpy(), oracle.linear_f64(dx, dw, bits(last)), dx, dw, k,
                 residual_f64(last, np.arange(3)), "last rows")
+
+
+def test_linears_at_once_on_two_streams():
+    """Every kernel of the linear on two streams at once, eight calls deep,
+    gives the bytes of calls alone: nothing is shared between calls."""
+    m = vq()
+    shapes = [(1280, 1024, 6144), (1024, 2560, 1024), (333, 1000, 1040), (8, 512, 2064), (64, 18952, 144)]
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    ops, want = [], []
+    for M, N, K in shapes:
+        kb, nb = -(-K // 128), -(-N // 128)
+        code = [torch.randint(0, 0x60, (r, K), generator=gen, device="cuda", dtype=torch.uint8) for r in (M, N)]
+        scale = [torch.rand(*s, generator=gen, device="cuda") for s in ((kb, M), (nb, kb))]
+        Y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+        ops.append((code[0], scale[0], code[1], scale[1], None, Y, M, N, K))
+        m.vlaq_linear_fp8_block(*ops[-1])
+        want.append(Y.clone())
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    twins = [o[:5] + (torch.empty_like(o[5]),) + o[6:] for o in ops]
+    for _ in range(8):
+        for i in range(len(ops)):
+            m.vlaq_linear_fp8_block(*ops[i], stream=a)
+            m.vlaq_linear_fp8_block(*twins[(i + 2) % len(ops)], stream=b)
+    torch.cuda.synchronize()
+    m.vlaq_check()
+    for o, t, w in zip(ops, twins, want):
+        assert torch.equal(o[5], w) and torch.equal(t[5], w), o[6:]
