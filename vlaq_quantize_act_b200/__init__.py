@@ -97,16 +97,24 @@ class VlaqError(RuntimeError):
 def _ptr(t):
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    try:
+        return t.data_ptr()  # first: a call passes up to ten tensors, and every check of each counts
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise
+
+
+_is_initialized = torch.cuda.is_initialized
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(stream):
     if stream is None:
-        if torch.cuda.is_initialized():
+        if _is_initialized():
             # the raw handle: building a Stream object took 3.9 us of a 9 us call
-            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+            return _raw_stream(_current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
