@@ -614,7 +614,7 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
 // elements (more CTAs, shorter chains; spread / in threads, us): 512 x 3584
 // (14336 blocks) 3.0 / 3.4, 1024 x 3584 (28672) 5.6 / 5.8, 8192 x 512 (32768) 6.1
 // / 6.0, 256 x 18944 (37888) 6.6 / 6.2, 1024 x 18944 (151552) 21.7 / 14.7.
-constexpr int64_t kFewBlocks = 30720;
+constexpr int64_t kFewBlocks = 30000;
 
 template <bool WEIGHT>
 cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
