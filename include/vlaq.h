@@ -359,6 +359,26 @@ VLAQ_API vlaq_status vlaq_quantize_act_fp8_block(const void* X, int64_t M, int64
 VLAQ_API vlaq_status vlaq_linear_fp8_block(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
                                   const void* residual, void* Y, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* What vlaq_linear_fp8_block runs for a shape (M >= 1) on the current device:
+ *   kernel  0: 128 weight rows x up to 64 tokens per tile; 1: 128 tokens x 128
+ *           weight rows; 2: 256 x 256 over CTA pairs
+ *   ctas    CTAs that share a tile: 1 to 8 (kernels 0, 1), 2 or 4 (kernel 2)
+ * Both are written on VLAQ_OK only. */
+VLAQ_API vlaq_status vlaq_linear_fp8_block_plan(int64_t M, int64_t N, int64_t K, int32_t* kernel, int32_t* ctas);
+
+/* Self test: vlaq_linear_fp8_block by the given kernel and CTAs per tile
+ * instead of the planned ones (M >= 1; kernel 0 holds at most 64 tokens, every
+ * CTA of a tile needs a block of 128 along K).
+ * With starve != 0 the token tiles arrive incomplete: the kernel's bounded
+ * waits run out after about 1 ms, it lets its copies in flight land and returns
+ * (about 3 ms in all); Y holds NaN where CTAs share a tile in kernels 0 and 1
+ * and is left as it was elsewhere; the next vlaq_check(stream) returns
+ * VLAQ_ERR_TIMEOUT, the one after it VLAQ_OK. */
+VLAQ_API vlaq_status vlaq_selftest_linear_fp8_block(int32_t kernel, int32_t ctas, int32_t starve, const uint8_t* xq,
+                                           const float* s_x, const uint8_t* wq, const float* s_w,
+                                           const void* residual, void* Y, int64_t M, int64_t N, int64_t K,
+                                           void* stream);
+
 /* ---------------------------------------------------------- residual norm */
 /* What runs between one block's output projection and the next block's
  * input projection, in one pass over the row:

@@ -462,30 +462,60 @@ vlaq_status vlaq_quantize_act_fp8_block(const void* X, int64_t M, int64_t K, con
   return ok();
 }
 
+// The checks of a block linear call with M > 0.
+static vlaq_status check_block_linear(const char* fn, const vlaq::BlockLinear& l) {
+  const void *xq = l.xq, *s_x = l.s_x, *wq = l.wq, *s_w = l.s_w, *Y = l.Y;
+  VLAQ_NONNULL(fn, xq);
+  VLAQ_NONNULL(fn, s_x);
+  VLAQ_NONNULL(fn, wq);
+  VLAQ_NONNULL(fn, s_w);
+  VLAQ_NONNULL(fn, Y);
+  if (l.residual && !aligned16(l.residual)) return fail(VLAQ_ERR_ALIGN, "%s: residual is not 16-byte aligned", fn);
+  return check_device(fn);
+}
+
 vlaq_status vlaq_linear_fp8_block(const uint8_t* xq, const float* s_x, const uint8_t* wq, const float* s_w,
                                   const void* residual, void* Y, int64_t M, int64_t N, int64_t K, void* stream) {
   const char* fn = "vlaq_linear_fp8_block";
   vlaq_status st;
   if ((st = check_linear_shape(fn, false, M, N, K))) return st;
   if (M == 0) return ok();
-  VLAQ_NONNULL(fn, xq);
-  VLAQ_NONNULL(fn, s_x);
-  VLAQ_NONNULL(fn, wq);
-  VLAQ_NONNULL(fn, s_w);
-  VLAQ_NONNULL(fn, Y);
-  if (residual && !aligned16(residual)) return fail(VLAQ_ERR_ALIGN, "%s: residual is not 16-byte aligned", fn);
+  const vlaq::BlockLinear l = {xq, s_x, wq, s_w, residual, Y, M, N, K, false};
+  if ((st = check_block_linear(fn, l))) return st;
+  cudaError_t e =
+      vlaq::launch_linear_fp8_block(l, vlaq::plan_linear_fp8_block(M, N, K), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
+vlaq_status vlaq_linear_fp8_block_plan(int64_t M, int64_t N, int64_t K, int32_t* kernel, int32_t* ctas) {
+  const char* fn = "vlaq_linear_fp8_block_plan";
+  vlaq_status st;
+  if ((st = check_linear_shape(fn, false, M, N, K))) return st;
+  if (M == 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = 0 runs no kernel", fn);
+  if (!kernel || !ctas) return fail(VLAQ_ERR_INVALID_ARG, "%s: %s is NULL", fn, kernel ? "ctas" : "kernel");
   if ((st = check_device(fn))) return st;
-  vlaq::BlockLinear l = {};
-  l.xq = xq;
-  l.s_x = s_x;
-  l.wq = wq;
-  l.s_w = s_w;
-  l.residual = residual;
-  l.Y = Y;
-  l.M = M;
-  l.N = N;
-  l.K = K;
-  cudaError_t e = vlaq::launch_linear_fp8_block(l, vlaq::kWaitBudgetCycles, static_cast<cudaStream_t>(stream));
+  const vlaq::BlockPlan plan = vlaq::plan_linear_fp8_block(M, N, K);
+  *kernel = plan.kernel;
+  *ctas = plan.ctas;
+  return ok();
+}
+
+vlaq_status vlaq_selftest_linear_fp8_block(int32_t kernel, int32_t ctas, int32_t starve, const uint8_t* xq,
+                                           const float* s_x, const uint8_t* wq, const float* s_w,
+                                           const void* residual, void* Y, int64_t M, int64_t N, int64_t K,
+                                           void* stream) {
+  const char* fn = "vlaq_selftest_linear_fp8_block";
+  vlaq_status st;
+  if ((st = check_linear_shape(fn, false, M, N, K))) return st;
+  if (M == 0) return fail(VLAQ_ERR_INVALID_ARG, "%s: M = 0 runs no kernel", fn);
+  const vlaq::BlockPlan plan = {kernel, ctas};
+  if (!vlaq::block_plan_valid(plan, M, K))
+    return fail(VLAQ_ERR_INVALID_ARG, "%s: kernel %d with %d CTAs per tile cannot run M = %lld, K = %lld", fn, kernel,
+                ctas, (long long)M, (long long)K);
+  const vlaq::BlockLinear l = {xq, s_x, wq, s_w, residual, Y, M, N, K, starve != 0};
+  if ((st = check_block_linear(fn, l))) return st;
+  cudaError_t e = vlaq::launch_linear_fp8_block(l, plan, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(fn, e);
   return ok();
 }

@@ -24,8 +24,12 @@
 // order of K: no workspace and the same result every time.
 //
 // Every mbarrier wait is bounded (clock budget); a wait that runs out sets a
-// shared abort flag and the device status word, the roles drain their own
-// in-flight copies and MMAs, TMEM is freed and the kernel returns.
+// shared abort flag and the device status word, and the roles stop.  Once all of
+// them have, a CTA that gave up stays until its copies in flight have landed
+// (let_copies_land), frees its TMEM and returns.  Tiles that were given up are
+// not stored, or, where a cluster of the rows and columns kernels adds the sums
+// of its CTAs, stored as NaN: the flags of the other CTAs cost 0.1 to 0.3 us of
+// every call to ask for.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -86,6 +90,26 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, lon
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long budget, volatile int* abort_flag,
                                           uint32_t peer_abort) {
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, budget, abort_flag, peer_abort));
+}
+
+// Time for the copies in flight of a CTA that gave up (of both CTAs of a pair,
+// whose copies signal the leader's barriers): they may still write its shared
+// memory and its barriers, and no barrier says when they have (a stage's also
+// counts the epilogue warps, which may never arrive).  A load takes a few us;
+// this is about 1 ms.  A CTA leaves after it, and after all its roles have
+// stopped; the abort flag is final then.
+__device__ __forceinline__ void let_copies_land() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1ll << 21)) {
+  }
+  __syncwarp();
+}
+
+// A thread's n sums of a tile that was given up, for the CTAs that add them:
+// not numbers, once no copy writes over them any more.
+__device__ __noinline__ void give_up_sums(float* sums, int n, int stride) {
+  let_copies_land();
+  for (int j = 0; j < n; ++j) sums[j * stride] = __int_as_float(0x7FFFFFFF);
 }
 
 // Values computed here, not where they are first used.
@@ -169,18 +193,12 @@ __device__ __forceinline__ void store4(const BlockArgs& a, float4 y, int m, int 
   *reinterpret_cast<uint2*>(a.Y + o) = make_uint2(bf16x2(y.x, y.y), bf16x2(y.z, y.w));
 }
 
-// Y[m, n .. n + 3] = bf16(sum over the cluster's CTAs, in rank order, of the
-// four fp32 sums at shared address `at` + residual).
-__device__ __forceinline__ void store_summed4(const BlockArgs& a, uint32_t at, int ctas, int m, int n) {
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int r = 0; r < ctas; ++r) {
-    const float4 v = ld_shared_cluster_f4(mapa_shared(at, r));
-    y.x += v.x;
-    y.y += v.y;
-    y.z += v.z;
-    y.w += v.w;
-  }
-  store4(a, y, m, n);
+// y += v.
+__device__ __forceinline__ void add4(float4& y, const float4& v) {
+  y.x += v.x;
+  y.y += v.y;
+  y.z += v.z;
+  y.w += v.w;
 }
 
 // Sums of the rows kernel's clusters: rows of 128 fp32 columns, 16-byte
@@ -347,18 +365,10 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
           }
         }
       }
-      if (ok) {
-        // the leader's last commits have landed in this CTA
-        for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
-          bounded_wait(&done_bar[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, a.budget, &s_abort,
-                       peer_abort);
-      } else {
-        // a stage that was given up may never complete: give every copy in
-        // flight the time to land before the pair's final barrier
-        const long long t0 = clock64();
-        while (clock64() - t0 < (1ll << 21)) {
-        }
-      }
+      // the leader's last commits have landed in this CTA (unless a wait gives up)
+      for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it && ok; ++i)
+        ok = bounded_wait(&done_bar[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, a.budget, &s_abort,
+                          peer_abort);
     } else if (warp == 1 && rank == 0 && elect_one()) {
       // ------------------------------------------------- MMA issuer (leader)
       const uint64_t xd = sdesc_kmajor_sw128(smem_u32(smem)), wd = sdesc_kmajor_sw128(smem_u32(smem) + kTileBytes);
@@ -404,7 +414,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     const uint32_t tbase = tmem + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(C::COLS * h);
     uint8_t* out = smem + C::STAGES * C::STAGE_BYTES + (warp - 4) * 2 * C::OUT_BYTES;
     uint32_t res_phase = 0;
-    bool loading = false;  // a residual load in flight
     int stage = 0;
     float* slots = &s_sx[0][threadIdx.x - 128];
     uint32_t phase = 0, buf = 0;
@@ -422,7 +431,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
         tma_load_2d(out + C::OUT_BYTES, &tmR, &res_bar[warp - 4], col0 + 64, row0);
       }
-      loading = a.residual && stores;
       // rows and columns past the output use the last ones' scales and are not stored
       ScaleStream<32 * C::EPI_WARPS> scales;
       scales.start(a.sx + static_cast<int64_t>(kb0) * a.M + min(row0 + lane, a.M - 1),
@@ -465,6 +473,8 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         cluster_sync();
         if (!stores) break;
         if (ok) {
+          const uint32_t gave_up =
+              ld_shared_cluster_u32(mapa_shared(smem_u32(const_cast<const int*>(&s_abort)), cta ^ 2u));
           const uint32_t other = mapa_shared(sums, cta ^ 2u);
 #pragma unroll
           for (int c = 0; c < C::COLS; c += 2) {
@@ -472,6 +482,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
             acc[c] += v.x;
             acc[c + 1] += v.y;
           }
+          ok = __all_sync(0xffffffffu, gave_up == 0);
         }
       }
       if (!ok) break;
@@ -481,7 +492,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       if (a.residual) {
         if (!warp_wait(&res_bar[warp - 4], res_phase, a.budget, &s_abort, peer_abort)) break;
         res_phase ^= 1u;
-        loading = false;
       } else {
         if (lane == 0) bulk_wait_group_read0();
         __syncwarp();
@@ -509,12 +519,6 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         bulk_commit_group();
       }
     }
-    if (loading) {
-      // the tile was given up: let its residual land before teardown
-      const long long t0 = clock64();
-      while (!mbar_try_wait(&res_bar[warp - 4], res_phase) && clock64() - t0 < (1ll << 21)) {
-      }
-    }
     if (lane == 0) bulk_wait_group0();
   }
 
@@ -524,6 +528,7 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   __syncwarp();
   if (SPLIT && warp < 4) cluster_sync_relaxed();  // (the epilogue warps' exchange of sums)
   cluster_sync();
+  if (s_abort) let_copies_land();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemColumns);
@@ -642,13 +647,6 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         }
       }
     }
-    if (!ok) {
-      // a stage that was given up may never complete: give every copy in
-      // flight the time to land before teardown
-      const long long t0 = clock64();
-      while (clock64() - t0 < (1ll << 21)) {
-      }
-    }
   } else if (warp == 1 && elect_one()) {
     // ----------------------------------------------------------- MMA issuer
     const uint64_t xd = sdesc_kmajor_sw128(smem_u32(smem)), wd = sdesc_kmajor_sw128(smem_u32(smem) + kTileBytes);
@@ -693,7 +691,6 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
     float* slots = &s_sx[0][threadIdx.x - 128];
     uint8_t* out = smem + C::STAGES * C::STAGE_BYTES + (warp - 4) * C::OUT_BYTES;
     uint32_t res_phase = 0;
-    bool loading = false;  // a residual load in flight
     int stage = 0;
     uint32_t phase = 0, buf = 0;
     bool ok = true;
@@ -701,13 +698,10 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
       const int row0 = (u % a.m_tiles) * C::BM + 32 * q;
       const int col0 = (u / a.m_tiles) * C::BN + C::COLS * h;
       const bool live = row0 < a.M && col0 < a.N;  // warp-uniform
-      if (a.residual && splits == 1) {
-        if (lane == 0) {
-          bulk_wait_group_read0();
-          mbar_arrive_expect_tx(&res_bar[warp - 4], C::OUT_BYTES);
-          tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
-        }
-        loading = true;
+      if (a.residual && splits == 1 && lane == 0) {
+        bulk_wait_group_read0();
+        mbar_arrive_expect_tx(&res_bar[warp - 4], C::OUT_BYTES);
+        tma_load_2d(out, &tmR, &res_bar[warp - 4], col0, row0);
       }
       // rows and columns past the output use the last ones' scales and are not stored
       const int n = kb1 - kb0;
@@ -752,7 +746,6 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         if (a.residual) {
           if (!warp_wait(&res_bar[warp - 4], res_phase, a.budget, &s_abort, 0)) break;
           res_phase ^= 1u;
-          loading = false;
         } else {
           if (lane == 0) bulk_wait_group_read0();
           __syncwarp();
@@ -780,12 +773,8 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
         }
       }
     }
-    if (loading) {
-      // the tile was given up: let its residual land before teardown
-      const long long t0 = clock64();
-      while (!mbar_try_wait(&res_bar[warp - 4], res_phase) && clock64() - t0 < (1ll << 21)) {
-      }
-    }
+    if (!ok && splits > 1)  // the permuted groups of a warp's columns stay in their half of the row
+      give_up_sums(reinterpret_cast<float*>(smem) + (32 * q + lane) * C::BN + C::COLS * h, C::COLS, 1);
     if (lane == 0) bulk_wait_group0();
   }
 
@@ -793,27 +782,24 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
   __syncwarp();
   if (splits > 1) {
     cluster_sync();  // every CTA's sums are in its shared memory
+    const int gave_up = s_abort;
     const int m0 = (group % a.m_tiles) * C::BM, n0 = (group / a.m_tiles) * C::BN;
-    const int rows = min(C::BM, a.M - m0);
+    const int items = min(C::BM, a.M - m0) * (C::BN / 4);
     const uint32_t sums = smem_u32(smem);
     // four columns of Y per item, added in the order of the blocks
-    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < rows * (C::BN / 4); i += splits * C::THREADS) {
+    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < items; i += splits * C::THREADS) {
       const int j = i / (C::BN / 4), c = i % (C::BN / 4), n = n0 + 4 * c;
       if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
       float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int r = 0; r < splits; ++r) {
-        const float4 v = read_sums(mapa_shared(sums, r), j, c);
-        y.x += v.x;
-        y.y += v.y;
-        y.z += v.z;
-        y.w += v.w;
-      }
+      for (int r = 0; r < splits; ++r) add4(y, read_sums(mapa_shared(sums, r), j, c));
       store4(a, y, m0 + j, n);
     }
     __syncwarp();
     cluster_sync_relaxed();  // no CTA leaves while another reads its sums
+    if (gave_up) let_copies_land();
   } else {
     __syncthreads();
+    if (s_abort) let_copies_land();
   }
   if (warp == 1) {
     tc_fence_after();
@@ -923,11 +909,6 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
           stage = 0;
           phase ^= 1u;
         }
-      }
-    }
-    if (!ok) {
-      const long long t0 = clock64();
-      while (clock64() - t0 < (1ll << 21)) {
       }
     }
   } else if (warp == 1 && elect_one()) {
@@ -1059,24 +1040,32 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
           if (j < a.M) a.Y[static_cast<size_t>(j) * a.N + n] = __float2bfloat16_rn(acc[j]);
       }
     }
+    if (!ok && splits > 1) give_up_sums(reinterpret_cast<float*>(smem) + 32 * q + lane, NT, C::BN);
   }
 
   tc_fence_before();
   __syncwarp();
   if (splits > 1) {
     cluster_sync();  // every CTA's sums are in its shared memory
+    const int gave_up = s_abort;
     const int n0 = group * C::BN;
+    const int items = a.M * (C::BN / 4);
     const uint32_t sums = smem_u32(smem);
     // four columns of Y per item, added in the order of the blocks
-    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < a.M * (C::BN / 4); i += splits * C::THREADS) {
+    for (int i = rank * C::THREADS + static_cast<int>(threadIdx.x); i < items; i += splits * C::THREADS) {
       const int j = i / (C::BN / 4), n = n0 + 4 * (i % (C::BN / 4));
       if (n >= a.N) continue;  // N % 8 == 0: four columns are in or out as a whole
-      store_summed4(a, sums + static_cast<uint32_t>(i) * 16u, splits, j, n);
+      float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int r = 0; r < splits; ++r)
+        add4(y, ld_shared_cluster_f4(mapa_shared(sums + static_cast<uint32_t>(i) * 16u, r)));
+      store4(a, y, j, n);
     }
     __syncwarp();
     cluster_sync_relaxed();  // no CTA leaves while another reads its sums
+    if (gave_up) let_copies_land();
   } else {
     __syncthreads();
+    if (s_abort) let_copies_land();
   }
   if (warp == 1) {
     tc_fence_after();
@@ -1087,7 +1076,7 @@ gemm_block_cols_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 // -------------------------------------------------------------- host side --
 constexpr int kMaxSplits = 8;  // portable cluster size
 
-BlockArgs make_block_args(const BlockLinear& l, int bm, int bn, long long budget) {
+BlockArgs make_block_args(const BlockLinear& l, int bm, int bn) {
   BlockArgs a;
   a.sx = l.s_x;
   a.sw = l.s_w;
@@ -1099,13 +1088,15 @@ BlockArgs make_block_args(const BlockLinear& l, int bm, int bn, long long budget
   a.m_tiles = static_cast<int>((l.M + bm - 1) / bm);
   a.n_tiles = static_cast<int>((l.N + bn - 1) / bn);
   a.units = a.m_tiles * a.n_tiles;
-  a.budget = budget;
+  a.budget = l.starve ? kStarvedBudgetCycles : kWaitBudgetCycles;
   return a;
 }
 
+// l.starve: boxes of half the token rows, so that no stage ever has all its
+// bytes and every wait for one runs out (the failure self test).
 bool make_block_maps(const BlockLinear& l, uint32_t x_rows, CUtensorMap* tx, CUtensorMap* tw) {
   const uint64_t k = static_cast<uint64_t>(l.K);
-  return make_map(tx, l.xq, k, static_cast<uint64_t>(l.M), k, x_rows) &&
+  return make_map(tx, l.xq, k, static_cast<uint64_t>(l.M), k, l.starve ? x_rows / 2 : x_rows) &&
          make_map(tw, l.wq, k, static_cast<uint64_t>(l.N), k, 128);
 }
 
@@ -1192,14 +1183,14 @@ cudaError_t launch_tiles(Kernel kern, int threads, int smem, int units, int spli
                             args..., splits);
 }
 
-cudaError_t run_block_pair(const BlockLinear& l, bool split, long long budget, cudaStream_t s) {
+cudaError_t run_block_pair(const BlockLinear& l, bool split, cudaStream_t s) {
   using C = PairTile;
   CUtensorMap tx, tw, ty, tr;
   const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
   if (!make_block_maps(l, 128, &tx, &tw) || !make_out_map(&ty, l.Y, cols, rows)) return cudaErrorInvalidValue;
   tr = ty;  // not read without a residual
   if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
-  const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
+  const BlockArgs a = make_block_args(l, C::BM, C::BN);
   auto kern = split ? gemm_block_pair_kernel<true> : gemm_block_pair_kernel<false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
@@ -1210,25 +1201,24 @@ cudaError_t run_block_pair(const BlockLinear& l, bool split, long long budget, c
                             C::SMEM_BYTES, s, tx, tw, ty, tr, a);
 }
 
-cudaError_t run_block_rows(const BlockLinear& l, int splits, long long budget, cudaStream_t s) {
+cudaError_t run_block_rows(const BlockLinear& l, int splits, cudaStream_t s) {
   using C = RowsTile;
   CUtensorMap tx, tw, ty, tr;
   const uint64_t cols = static_cast<uint64_t>(l.N), rows = static_cast<uint64_t>(l.M);
   if (!make_block_maps(l, C::BM, &tx, &tw) || !make_out_map(&ty, l.Y, cols, rows)) return cudaErrorInvalidValue;
   tr = ty;  // not read without a residual
   if (l.residual && !make_out_map(&tr, const_cast<void*>(l.residual), cols, rows)) return cudaErrorInvalidValue;
-  const BlockArgs a = make_block_args(l, C::BM, C::BN, budget);
+  const BlockArgs a = make_block_args(l, C::BM, C::BN);
   return launch_tiles(gemm_block_rows_kernel, C::THREADS, C::SMEM_BYTES, a.units, splits, s, tx, tw, ty, tr, a);
 }
 
 template <int NT>
-cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t s) {
+cudaError_t run_block_cols(const BlockLinear& l, int splits, cudaStream_t s) {
   using C = ColsTile<NT>;
   CUtensorMap tx, tw;
   if (!make_block_maps(l, NT, &tx, &tw)) return cudaErrorInvalidValue;
-  const BlockArgs a = make_block_args(l, NT, C::BN, budget);
-  return launch_tiles(gemm_block_cols_kernel<NT>, C::THREADS, C::SMEM_BYTES, a.units,
-                      choose_splits(a.units, a.blocks, cols_clusters<NT>), s, tx, tw, a);
+  const BlockArgs a = make_block_args(l, NT, C::BN);
+  return launch_tiles(gemm_block_cols_kernel<NT>, C::THREADS, C::SMEM_BYTES, a.units, splits, s, tx, tw, a);
 }
 
 }  // namespace
@@ -1248,16 +1238,18 @@ cudaError_t run_block_cols(const BlockLinear& l, long long budget, cudaStream_t 
 // constants are fits to 110 shapes of 65 to 4580 tokens, widths to 37888 and
 // depths to 18944; the plan chosen took 1.3% longer than the best on average, 19%
 // at most.
-cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s) {
-  if (l.M <= 16) return run_block_cols<16>(l, budget, s);
-  if (l.M <= 32) return run_block_cols<32>(l, budget, s);
-  const int64_t blocks = (l.K + 127) / 128;
-  const int64_t units = ceil_div(l.M, 256) * ceil_div(l.N, 256), tiles = ceil_div(l.M, 128) * ceil_div(l.N, 128);
+BlockPlan plan_linear_fp8_block(int64_t M, int64_t N, int64_t K) {
+  const int64_t blocks = ceil_div(K, 128);
+  const int64_t columns = ceil_div(N, 128), tiles = ceil_div(M, 128) * columns;
+  if (M <= 16) return {kBlockCols, choose_splits(columns, blocks, cols_clusters<16>)};
+  if (M <= 32) return {kBlockCols, choose_splits(columns, blocks, cols_clusters<32>)};
   int splits = choose_splits(tiles, blocks, rows_clusters);
-  if (l.M <= 64) {
+  if (M <= 64) {
     const int64_t in_a_row = ceil_div(tiles, splits > 1 ? tiles : device_sm_count()) * ceil_div(blocks, splits);
-    return in_a_row <= 20 ? run_block_cols<64>(l, budget, s) : run_block_rows(l, splits, budget, s);
+    if (in_a_row <= 20) return {kBlockCols, choose_splits(columns, blocks, cols_clusters<64>)};
+    return {kBlockRows, splits};
   }
+  const int64_t units = ceil_div(M, 256) * ceil_div(N, 256);
   const int64_t pair = 2700 + ceil_div(units, pair_clusters(false)) * (1800 + 455 * blocks);
   const int64_t halves = ceil_div(units, pair_clusters(true)) * (8600 + 245 * blocks) - 1500;
   int64_t rows = 2600 + ceil_div(tiles, device_sm_count()) * (1000 + kBlockNs * blocks);
@@ -1265,8 +1257,23 @@ cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cuda
     rows = split_ns(blocks, splits);
   else
     splits = 1;
-  if (rows <= pair && rows <= halves) return run_block_rows(l, splits, budget, s);
-  return run_block_pair(l, blocks > 1 && halves < pair, budget, s);
+  if (rows <= pair && rows <= halves) return {kBlockRows, splits};
+  return {kBlockPair, blocks > 1 && halves < pair ? 4 : 2};
+}
+
+bool block_plan_valid(const BlockPlan& plan, int64_t M, int64_t K) {
+  const int64_t blocks = ceil_div(K, 128);
+  if (plan.kernel == kBlockPair) return plan.ctas == 2 || (plan.ctas == 4 && blocks >= 2);
+  if (plan.kernel != kBlockRows && (plan.kernel != kBlockCols || M > 64)) return false;
+  return plan.ctas >= 1 && plan.ctas <= kMaxSplits && plan.ctas <= blocks;
+}
+
+cudaError_t launch_linear_fp8_block(const BlockLinear& l, const BlockPlan& plan, cudaStream_t s) {
+  if (plan.kernel == kBlockPair) return run_block_pair(l, plan.ctas == 4, s);
+  if (plan.kernel == kBlockRows) return run_block_rows(l, plan.ctas, s);
+  if (l.M <= 16) return run_block_cols<16>(l, plan.ctas, s);
+  if (l.M <= 32) return run_block_cols<32>(l, plan.ctas, s);
+  return run_block_cols<64>(l, plan.ctas, s);
 }
 
 cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s) {

@@ -18,6 +18,8 @@ constexpr int64_t kMaxQuantK = 32768;
 
 // Clock-cycle limit of every bounded wait in the library kernels (~1 s).
 constexpr long long kWaitBudgetCycles = 2000000000LL;
+// The same in the failure self tests, whose waits are meant to run out (~1 ms).
+constexpr long long kStarvedBudgetCycles = 2000000LL;
 
 constexpr uint32_t kFlagRmsNorm = 1u;
 constexpr uint32_t kFlagHadamard = 2u;
@@ -98,8 +100,19 @@ struct BlockLinear {
   const void* residual;
   void* Y;
   int64_t M, N, K;
+  bool starve;  // failure self test: token tiles arrive incomplete, waits run out after kStarvedBudgetCycles
 };
-cudaError_t launch_linear_fp8_block(const BlockLinear& l, long long budget, cudaStream_t s);
+// Kernel of a call and the CTAs that share a tile (kBlockPair: 2 or 4, else 1
+// to 8): the fastest by estimate on the current device.
+enum : int { kBlockCols = 0, kBlockRows = 1, kBlockPair = 2 };
+struct BlockPlan {
+  int kernel, ctas;
+};
+BlockPlan plan_linear_fp8_block(int64_t M, int64_t N, int64_t K);
+// Whether the kernels can run it (kBlockCols holds at most 64 tokens; every CTA
+// of a tile needs a block of K).
+bool block_plan_valid(const BlockPlan& plan, int64_t M, int64_t K);
+cudaError_t launch_linear_fp8_block(const BlockLinear& l, const BlockPlan& plan, cudaStream_t s);
 struct ResidualNorm {
   const void* H;
   const void* Y;
