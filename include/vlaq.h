@@ -109,7 +109,7 @@ VLAQ_API const char* vlaq_last_error(void);
 /* Library version, major * 10000 + minor * 100 + patch. */
 VLAQ_API int vlaq_version(void);
 
-/* Synchronizes `stream`, then reads and clears the device status word of
+/* Synchronizes `stream`, then reads and clears the device status words of
  * the current device.  Returns VLAQ_ERR_TIMEOUT if a kernel gave up a
  * bounded wait since the last check, VLAQ_ERR_CUDA on a CUDA error. */
 VLAQ_API vlaq_status vlaq_check(void* stream);

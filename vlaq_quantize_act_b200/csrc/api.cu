@@ -128,17 +128,6 @@ vlaq_status vlaq_check(void* stream) {
   unsigned int st = 0;
   cudaError_t e = vlaq::read_and_clear_status(&st, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
-  unsigned int qst = 0;
-  e = vlaq::read_and_clear_quant_status(&qst, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
-  st |= qst;
-  unsigned int bst = 0;
-  e = vlaq::read_and_clear_block_status(&bst, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
-  st |= bst;
-  e = vlaq::read_and_clear_block128_status(&bst, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail("vlaq_check", e);
-  st |= bst;
   if (st & vlaq::kStatusTimeout) {
     // a GEMM that gave up may have left split-K tile counters non-zero
     e = vlaq::noalloc_clear(static_cast<cudaStream_t>(stream));

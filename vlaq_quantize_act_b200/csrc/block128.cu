@@ -683,16 +683,8 @@ cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, u
                     static_cast<const __nv_bfloat16*>(W), N, K, codes, s_w);
 }
 
-cudaError_t read_and_clear_block128_status(unsigned int* out, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_block128_status, sizeof(unsigned int), 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_vlaq_block128_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
-  if (e != cudaSuccess) return e;
-  return cudaStreamSynchronize(s);
+cudaError_t block_quant_status_word(unsigned int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_vlaq_block128_status);
 }
 
 cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s) {

@@ -2056,16 +2056,8 @@ cudaError_t launch_linear_int8(const int8_t* xq, const float* s_x, const int8_t*
   return run_fp8<128, true>(x8, s_x, w8, s_w, residual, Y, M, N, K, workspace, plan, budget, s);
 }
 
-cudaError_t read_and_clear_status(unsigned int* out, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_status, sizeof(unsigned int), 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_vlaq_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
-  if (e != cudaSuccess) return e;
-  return cudaStreamSynchronize(s);
+cudaError_t gemm_status_word(unsigned int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_vlaq_status);
 }
 
 int device_sm_count() {

@@ -1276,16 +1276,8 @@ cudaError_t launch_linear_fp8_block(const BlockLinear& l, const BlockPlan& plan,
   return run_block_cols<64>(l, plan.ctas, s);
 }
 
-cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_block_status, sizeof(unsigned int), 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_vlaq_block_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
-  if (e != cudaSuccess) return e;
-  return cudaStreamSynchronize(s);
+cudaError_t block_linear_status_word(unsigned int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_vlaq_block_status);
 }
 
 }  // namespace vlaq

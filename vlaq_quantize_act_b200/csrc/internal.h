@@ -131,11 +131,13 @@ struct ResidualNorm {
 };
 cudaError_t launch_residual_norm(const ResidualNorm& r, cudaStream_t s);
 
-// Device status word accessors (gemm.cu, quant.cu, gemm_block.cu, block128.cu).
+// Device addresses of the status words (gemm.cu, quant.cu, gemm_block.cu,
+// block128.cu), and all of them read and cleared (status.cu).
+cudaError_t gemm_status_word(unsigned int** out);
+cudaError_t quant_status_word(unsigned int** out);
+cudaError_t block_linear_status_word(unsigned int** out);
+cudaError_t block_quant_status_word(unsigned int** out);
 cudaError_t read_and_clear_status(unsigned int* out, cudaStream_t s);
-cudaError_t read_and_clear_quant_status(unsigned int* out, cudaStream_t s);
-cudaError_t read_and_clear_block_status(unsigned int* out, cudaStream_t s);
-cudaError_t read_and_clear_block128_status(unsigned int* out, cudaStream_t s);
 cudaError_t launch_selftest_wait_timeout(cudaStream_t s);
 
 // Kernel launch with the programmatic-stream-serialization attribute, so the

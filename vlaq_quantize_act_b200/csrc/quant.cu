@@ -559,16 +559,8 @@ cudaError_t launch_selftest_wait_timeout(cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t read_and_clear_quant_status(unsigned int* out, cudaStream_t s) {
-  cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_vlaq_quant_status, sizeof(unsigned int), 0,
-                                            cudaMemcpyDeviceToHost, s);
-  if (e != cudaSuccess) return e;
-  e = cudaStreamSynchronize(s);
-  if (e != cudaSuccess) return e;
-  const unsigned int zero = 0;
-  e = cudaMemcpyToSymbolAsync(g_vlaq_quant_status, &zero, sizeof(unsigned int), 0, cudaMemcpyHostToDevice, s);
-  if (e != cudaSuccess) return e;
-  return cudaStreamSynchronize(s);
+cudaError_t quant_status_word(unsigned int** out) {
+  return cudaGetSymbolAddress(reinterpret_cast<void**>(out), g_vlaq_quant_status);
 }
 
 }  // namespace vlaq
