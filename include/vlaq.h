@@ -379,6 +379,14 @@ VLAQ_API vlaq_status vlaq_selftest_linear_fp8_block(int32_t kernel, int32_t ctas
                                            const void* residual, void* Y, int64_t M, int64_t N, int64_t K,
                                            void* stream);
 
+/* Self test: the rotated block quantizer for many blocks (activations, or a
+ * weight with weight != 0), whatever their number; rows >= 1.  With starve != 0
+ * its tiles arrive incomplete: the wait for the first one runs out after about
+ * 1 ms, codes and scales are left as they were, and vlaq_check reports it as
+ * above. */
+VLAQ_API vlaq_status vlaq_selftest_rotate_fp8_block(int32_t weight, int32_t starve, const void* X, int64_t rows, int64_t K,
+                                           uint8_t* codes, float* scales, void* stream);
+
 /* ---------------------------------------------------------- residual norm */
 /* What runs between one block's output projection and the next block's
  * input projection, in one pass over the row:

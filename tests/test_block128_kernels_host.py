@@ -50,3 +50,14 @@ def test_no_device_is_an_error(vq):  # noqa: F811
         with pytest.raises(vq.VlaqError) as ei:
             call()
         assert ei.value.status in (4, 5)
+
+
+def test_rotate_self_test_refuses_bad_calls(vq):  # noqa: F811
+    f = vq.vlaq_selftest_rotate_fp8_block
+    refused(vq, 2, lambda: f(0, 0, FAKE, 0, 256, FAKE, FAKE))
+    refused(vq, 2, lambda: f(0, 0, FAKE, 4, 96, FAKE, FAKE))
+    refused(vq, 2, lambda: f(1, 0, FAKE, 4, 32832, FAKE, FAKE))
+    for i in (2, 5, 6):
+        args = [1, 1, FAKE, 4, 256, FAKE, FAKE]
+        refused(vq, 1, lambda: f(*(None if j == i else a for j, a in enumerate(args))))
+        refused(vq, 3, lambda: f(*(FAKE + 8 if j == i else a for j, a in enumerate(args))))

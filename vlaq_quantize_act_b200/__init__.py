@@ -26,7 +26,7 @@ __all__ = [
     "vlaq_quantize_weight_fp8", "vlaq_quantize_act_fp8", "vlaq_linear_fp8", "vlaq_linear_nvfp4_noalloc",
     "vlaq_quantize_weight_int8", "vlaq_quantize_act_int8", "vlaq_linear_int8",
     "vlaq_quantize_weight_fp8_block", "vlaq_quantize_act_fp8_block", "vlaq_linear_fp8_block",
-    "vlaq_linear_fp8_block_plan", "vlaq_selftest_linear_fp8_block",
+    "vlaq_linear_fp8_block_plan", "vlaq_selftest_linear_fp8_block", "vlaq_selftest_rotate_fp8_block",
     "vlaq_residual_norm", "vlaq_residual_norm_fp8_block",
     "alloc_nvfp4", "alloc_fp8", "alloc_fp8_block", "alloc_int8", "alloc_workspace",
 ]
@@ -82,6 +82,7 @@ _SIGS = {
                                                   ctypes.POINTER(ctypes.c_int32)]),
     "vlaq_selftest_linear_fp8_block": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P,
                                                       _P, _P, _I64, _I64, _I64, _P]),
+    "vlaq_selftest_rotate_fp8_block": (ctypes.c_int, [ctypes.c_int32, ctypes.c_int32, _P, _I64, _I64, _P, _P, _P]),
     "vlaq_residual_norm": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _F, _P, _P, _P]),
     "vlaq_residual_norm_fp8_block": (ctypes.c_int, [_P, _P, _I64, _I64, _P, _P, _I64, _F, _P, _F, _U32, _P, _P, _P,
                                                     _P]),
@@ -238,6 +239,11 @@ def vlaq_linear_fp8_block_plan(M, N, K):
 def vlaq_selftest_linear_fp8_block(kernel, ctas, starve, xq, s_x, wq, s_w, residual, Y, M, N, K, stream=None):
     _check(_lib.vlaq_selftest_linear_fp8_block(kernel, ctas, starve, _ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w),
                                                _ptr(residual), _ptr(Y), M, N, K, _stream(stream)))
+
+
+def vlaq_selftest_rotate_fp8_block(weight, starve, X, rows, K, codes, scales, stream=None):
+    _check(_lib.vlaq_selftest_rotate_fp8_block(weight, starve, _ptr(X), rows, K, _ptr(codes), _ptr(scales),
+                                               _stream(stream)))
 
 
 # --------------------------------------------------------- residual norm

@@ -451,6 +451,22 @@ vlaq_status vlaq_quantize_act_fp8_block(const void* X, int64_t M, int64_t K, con
   return ok();
 }
 
+vlaq_status vlaq_selftest_rotate_fp8_block(int32_t weight, int32_t starve, const void* X, int64_t rows, int64_t K,
+                                           uint8_t* codes, float* scales, void* stream) {
+  const char* fn = "vlaq_selftest_rotate_fp8_block";
+  vlaq_status st;
+  if ((st = check_k(fn, K, VLAQ_F_HADAMARD64, false, vlaq::kMaxQuantK))) return st;
+  if (rows <= 0 || rows > 0x7FFFFFFF) return fail(VLAQ_ERR_SHAPE, "%s: rows = %lld out of range", fn, (long long)rows);
+  VLAQ_NONNULL(fn, X);
+  VLAQ_NONNULL(fn, codes);
+  VLAQ_NONNULL(fn, scales);
+  if ((st = check_device(fn))) return st;
+  cudaError_t e = vlaq::launch_rotated_fp8_block(weight != 0, starve != 0, X, rows, K, codes, scales,
+                                                 static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(fn, e);
+  return ok();
+}
+
 // The checks of a block linear call with M > 0.
 static vlaq_status check_block_linear(const char* fn, const vlaq::BlockLinear& l) {
   const void *xq = l.xq, *s_x = l.s_x, *wq = l.wq, *s_w = l.s_w, *Y = l.Y;

@@ -616,11 +616,14 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
 // / 6.0, 256 x 18944 (37888) 6.6 / 6.2, 1024 x 18944 (151552) 21.7 / 14.7.
 constexpr int64_t kFewBlocks = 30000;
 
+// starve: boxes of half the rows, so that no tile ever has all its bytes and the
+// wait for it runs out (the failure self test).
 template <bool WEIGHT>
-cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, cudaStream_t s) {
+cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* codes, float* scales, bool starve,
+                           cudaStream_t s) {
   CUtensorMap map, out_map;
   const uint64_t cols = static_cast<uint64_t>(K);
-  if (!make_bf16_map(&map, X, cols, static_cast<uint64_t>(rows), 128) ||
+  if (!make_bf16_map(&map, X, cols, static_cast<uint64_t>(rows), starve ? 64 : 128) ||
       !make_map(&out_map, codes, cols, static_cast<uint64_t>(rows), cols, 128))
     return cudaErrorInvalidValue;
   RotArgs r;
@@ -630,7 +633,7 @@ cudaError_t launch_rotated(const void* X, int64_t rows, int64_t K, uint8_t* code
   r.k_blocks = static_cast<uint32_t>(k_blocks);
   r.tiles = static_cast<uint32_t>(tiles);
   r.scales = scales;
-  r.budget = kWaitBudgetCycles;
+  r.budget = starve ? kStarvedBudgetCycles : kWaitBudgetCycles;
   const cudaError_t e = cudaFuncSetAttribute(quant_rotated_kernel<WEIGHT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              kRotSmem);
   if (e != cudaSuccess) return e;
@@ -657,7 +660,7 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
     return wht ? launch_norm<false, true, kOutFp8>(a, s) : launch_norm<false, false, kOutFp8>(a, s);
   }
   const int64_t blocks = (K + 127) / 128;
-  if (wht && M * blocks > kFewBlocks) return launch_rotated<false>(X, M, K, codes, s_x, s);
+  if (wht && M * blocks > kFewBlocks) return launch_rotated<false>(X, M, K, codes, s_x, false, s);
   BlocksArgs a;
   a.X = static_cast<const __nv_bfloat16*>(X);
   a.rows = M;
@@ -676,11 +679,17 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
 
 cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
                                           float* s_w, cudaStream_t s) {
-  if (flags & kFlagHadamard) return launch_rotated<true>(W, N, K, codes, s_w, s);
+  if (flags & kFlagHadamard) return launch_rotated<true>(W, N, K, codes, s_w, false, s);
   const int64_t tiles = ((N + 127) / 128) * ((K + 127) / 128);
   if (tiles > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
   return launch_pdl(quant_weight_block_kernel, dim3(static_cast<unsigned int>(tiles)), dim3(kWeightThreads), 0, s,
                     static_cast<const __nv_bfloat16*>(W), N, K, codes, s_w);
+}
+
+cudaError_t launch_rotated_fp8_block(bool weight, bool starve, const void* X, int64_t rows, int64_t K, uint8_t* codes,
+                                     float* scales, cudaStream_t s) {
+  return weight ? launch_rotated<true>(X, rows, K, codes, scales, starve, s)
+                : launch_rotated<false>(X, rows, K, codes, scales, starve, s);
 }
 
 cudaError_t block_quant_status_word(unsigned int** out) {

@@ -92,6 +92,9 @@ cudaError_t launch_quant_act_fp8_block(const void* X, int64_t M, int64_t K, cons
                                        uint32_t flags, uint8_t* codes, float* s_x, cudaStream_t s);
 cudaError_t launch_quant_weight_fp8_block(const void* W, int64_t N, int64_t K, uint32_t flags, uint8_t* codes,
                                           float* s_w, cudaStream_t s);
+// The rotation by tiles, whatever the number of blocks; starve: the failure self test.
+cudaError_t launch_rotated_fp8_block(bool weight, bool starve, const void* X, int64_t rows, int64_t K, uint8_t* codes,
+                                     float* scales, cudaStream_t s);
 struct BlockLinear {
   const uint8_t* xq;
   const float* s_x;
