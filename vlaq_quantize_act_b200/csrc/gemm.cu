@@ -29,8 +29,9 @@
 // global stores.
 //
 // Every mbarrier wait is bounded (clock budget); a wait that runs out sets a
-// shared abort flag and the device status word, the roles drain their own
-// in-flight copies and MMAs, TMEM is freed and the kernel returns.
+// shared abort flag and the device status word, and the roles stop.  Once all of
+// them have, a CTA that gave up stays until its copies in flight have landed
+// (let_copies_land), frees its TMEM and returns.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -520,6 +521,7 @@ gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
   tc_fence_before();
   __syncthreads();
+  if (s_abort) let_copies_land();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -972,6 +974,7 @@ gemm_fp4_sfw_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_consta
 
   tc_fence_before();
   __syncthreads();
+  if (s_abort) let_copies_land();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
@@ -1428,6 +1431,7 @@ gemm_fp4_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   tc_fence_before();
   __syncwarp();
   cluster_sync();
+  if (s_abort) let_copies_land();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
@@ -1709,6 +1713,7 @@ gemm_fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_const
   tc_fence_before();
   __syncwarp();
   cluster_sync();
+  if (s_abort) let_copies_land();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);

@@ -92,19 +92,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long l
   return __all_sync(0xffffffffu, bounded_wait(bar, parity, budget, abort_flag, peer_abort));
 }
 
-// Time for the copies in flight of a CTA that gave up (of both CTAs of a pair,
-// whose copies signal the leader's barriers): they may still write its shared
-// memory and its barriers, and no barrier says when they have (a stage's also
-// counts the epilogue warps, which may never arrive).  A load takes a few us;
-// this is about 1 ms.  A CTA leaves after it, and after all its roles have
-// stopped; the abort flag is final then.
-__device__ __forceinline__ void let_copies_land() {
-  const long long t0 = clock64();
-  while (clock64() - t0 < (1ll << 21)) {
-  }
-  __syncwarp();
-}
-
 // A thread's n sums of a tile that was given up, for the CTAs that add them:
 // not numbers, once no copy writes over them any more.
 __device__ __noinline__ void give_up_sums(float* sums, int n, int stride) {

@@ -107,6 +107,19 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, long l
   }
 }
 
+// Time for the copies in flight of a CTA that gave up (of both CTAs of a pair,
+// whose copies signal the leader's barriers): they may still write its shared
+// memory and its barriers, and no barrier says when they have (a stage's may
+// count warps that never arrive).  A load takes a few us; this is about 1 ms.
+// A CTA leaves after it, and it begins once all roles of the CTA have stopped:
+// the abort flag is final then and nothing more is issued.
+__device__ __forceinline__ void let_copies_land() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < (1ll << 21)) {
+  }
+  __syncwarp();
+}
+
 // ------------------------------------------- programmatic dependent launch --
 // Blocks until the grids this one depends on have completed and their memory
 // is visible (returns at once when the launch had no programmatic edge).
