@@ -13,9 +13,17 @@
 //   quant_rotated_kernel         one 64-element rotation per thread, tiles by TMA
 //   quant_weight_block_kernel    a CTA per 128 x 128 block, 64 elements a thread
 //   norm_rows_kernel             a CTA per row, 16-element chunks
-// All are bound by HBM for many rows (2 or 4 bytes in, 1 to 4 out per element;
-// the rotations by their instructions as well) and by the launch and one memory
-// round trip for one row.
+// For one row all are bound by the launch and one memory round trip.  For many
+// rows (2 or 4 bytes in, 1 to 4 out per element) the weight blocks and the bf16
+// residual norm are bound by HBM (5.8 to 6.4 TB/s; plain activation blocks 5.1 to
+// 5.3), the rotations by their instructions as well (5.1); rows with a norm and an
+// FP8 result by the chain of steps of a row, of which a CTA has one at a time:
+// 4580 x 3584 RMSNorm to FP8 18.2 us (2.7 TB/s), rotated 20.8, residual norm to
+// FP8 27.8 (4.1), rotated and gated 32.7.
+//
+// Times are device times of a call, in a CUDA graph of calls over buffers larger
+// than L2, where nothing else is said; a pair of times with an arrow is one
+// change, measured before and after it.
 //
 // Sums of squares use a fixed tree of 256 lanes, so a row's result does not
 // depend on how many rows the call has or on the CTA's thread count: lane l
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kWeightThreads, 4)
 // ahead; thread t has row t % 128 of box t / 128, so a quarter warp's 16-byte
 // reads fall on eight different swizzled positions; the codes leave by one
 // TMA store per tile (stored by the threads, 64 bytes of a row each, 37888 x
-// 3584 took 95 us).  37888 x 3584: 78.7 us, 5.2 TB/s; 1024 x 18944: 14.7 us.  Two
+// 3584 took 95 us).  37888 x 3584: 80 us, 5.1 TB/s; 1024 x 18944: 14.7 us.  Two
 // CTAs per SM (the 64 values of a thread) alternate between memory and the
 // about 500 instructions of 64 elements, of which the rotation has 220.
 constexpr int kRotThreads = 256;
@@ -484,8 +492,10 @@ __device__ __forceinline__ void scale_chunk(float* v, float s) {
 // 48 registers and 1280 threads for bf16 outputs (4580 x 3584: 22.7 us; 24.2 at
 // 60 registers), 64 and 1024 for FP8 ones, which spill at 48 (1024 x 3584: 10.6
 // against 10.9 us).  Two chunks: 80 and 768 (4000 x 8192: 50 us, 62 unbounded).
-// Four: 128 and 512, some forms spill 40 words (1024 x 16384 bf16 34.8 us, 43.4
-// unbounded; 54 us with the eight chunks of the longest rows).
+// Four: 128 and 512 (1024 x 16384 bf16 34.7 us, 43.4 unbounded; 54 us with the
+// eight chunks of the longest rows).  Eight: one CTA of 255.  All three residual
+// forms of four and of eight chunks spill, 35 to 47 words a thread; 2000 x 12288
+// to FP8 takes 56 us (3.1 TB/s), rotated 62.
 constexpr int norm_min_ctas(int threads, int chunks, int out) {
   return chunks == 1 ? (out == 0 ? 1280 : 1024) / threads : chunks == 2 ? 768 / threads : chunks == 4 ? 2 : 1;
 }
@@ -611,9 +621,10 @@ cudaError_t launch_norm(const NormArgs& a, cudaStream_t s) {
 }
 
 // Rotated 1 x 128 blocks of a call up to which they stay on 8 lanes per 64
-// elements (more CTAs, shorter chains; spread / in threads, us): 512 x 3584
-// (14336 blocks) 3.0 / 3.4, 1024 x 3584 (28672) 5.6 / 5.8, 8192 x 512 (32768) 6.1
-// / 6.0, 256 x 18944 (37888) 6.6 / 6.2, 1024 x 18944 (151552) 21.7 / 14.7.
+// elements (more CTAs, shorter chains; spread / in threads, us, buffers larger
+// than L2): 512 x 3584 (14336 blocks) 3.7 / 4.2, 1024 x 3584 (28672) 5.7 / 5.8,
+// 8192 x 512 (32768) 6.1 / 6.0, 256 x 18944 (37888) 6.6 / 6.3, 1024 x 18944
+// (151552) 21.7 / 14.7.
 constexpr int64_t kFewBlocks = 30000;
 
 // starve: boxes of half the rows, so that no tile ever has all its bytes and the

@@ -23,6 +23,10 @@
 // The CTAs of a cluster add their sums over each other's shared memory, in the
 // order of K: no workspace and the same result every time.
 //
+// Times are device times of a call, in a CUDA graph of calls over buffers larger
+// than L2, where nothing else is said; a pair of times with an arrow is one
+// change, measured before and after it.
+//
 // Every mbarrier wait is bounded (clock budget); a wait that runs out sets a
 // shared abort flag and the device status word, and the roles stop.  Once all of
 // them have, a CTA that gave up stays until its copies in flight have landed
@@ -232,9 +236,10 @@ __device__ __forceinline__ float4 read_sums(uint32_t base, int row, int group) {
 // (40), warps 4-11 take 232: 40 + 2 * 232 = 3 * 168 (the build checks that
 // ptxas allocates 168 at entry).
 //
-// What bounds it: the board's 1000 W.  1024 x 37888 x 3584 takes 148 us (1.88
-// PFLOP/s) at 1.43 GHz, 4580 x 3584 x 18944 348 us (1.79) at 1.46 GHz; the
-// per-row FP8 kernel, whose sums stay in TMEM, 131 and 298 us at 1.3 GHz, and
+// What bounds it: the board's 1000 W.  In a loop of seconds 1024 x 37888 x 3584
+// takes 153 us (1.82 PFLOP/s) at 1.38 GHz, 4580 x 3584 x 18944 357 us (1.74) at
+// 1.43 GHz (a first few calls, before the power limit acts, 133 and 314 us); the
+// per-row FP8 kernel, whose sums stay in TMEM, 132 and 299 us at 1.31 GHz, and
 // this kernel without its epilogue 285 us.  A block takes about 850 clocks of
 // which the MMA is 512: the rest is the round trip from commit to the epilogue
 // warps and back (about 420 clocks by itself) and the 32768 products of a
@@ -246,7 +251,7 @@ __device__ __forceinline__ float4 read_sums(uint32_t base, int row, int group) {
 // SPLIT: few tiles and a long K.  A cluster of two pairs has one tile, each pair
 // half of its blocks; then each CTA sends the sums of half of its columns to
 // the other pair's CTA of its rows and stores the other half.  512 x 3584 x
-// 18944 (28 tiles): 67 -> 43 us; the exchange and the start of the larger
+// 18944 (28 tiles): 64 -> 41 us; the exchange and the start of the larger
 // cluster cost about 3 us (reads of the other CTA's sums one row per lane, not
 // side by side: 8 us).
 struct PairTile {
@@ -535,8 +540,8 @@ gemm_block_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 //
 // What bounds it: a block takes about 310 ns (600 clocks) in a long K, of which
 // shared memory takes 512: 32 KB in by TMA and 32 KB out to the MMA, whose own
-// time is 256.  512 x 3584 x 3584: 12.3 us (112 tiles), 128 x 3584 x 3584 8.4
-// (28 tiles of five CTAs, HBM and the first stage), 333 x 1000 x 2000 7.2.
+// time is 256.  512 x 3584 x 3584: 12.4 us (112 tiles), 128 x 3584 x 3584 8.5
+// (28 tiles of four CTAs, HBM and the first stage), 333 x 1000 x 2000 7.2 (four).
 // Measured against it: epilogue warps in two sets that take alternate blocks,
 // 128 columns each, the same within 3%; four stages 12.5 us, prefetching
 // weights 6 or 12 blocks ahead 13.1.
@@ -802,8 +807,11 @@ gemm_block_rows_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_con
 // through shared memory, copied by the epilogue warps one chunk ahead.
 //
 // What bounds it: HBM for the weights, behind about 3 us of start, first round
-// trip and cluster sum.  8 x 3584 x 18944 14.4 us (4.7 TB/s), 4 x 37888 x 3584
-// 23.9 (5.7), 1 x 4608 x 3584 6.2.
+// trip and cluster sum.  8 x 3584 x 18944 14.4 us (28 tiles of four CTAs, 4.7
+// TB/s), 4 x 37888 x 3584 23.8 (296 tiles of one, 5.7), 1 x 4608 x 3584 6.4 (36
+// tiles of three).  Widths of 75 to 147 tiles do not fill the chip: tiles are
+// split only while all clusters are resident at once, so 1 x 10240 x 3584 runs
+// 80 CTAs and takes 11.3 us (3.3 TB/s).
 template <int NT>
 struct ColsTile {
   static constexpr int BN = 128;  // weight rows
@@ -1140,8 +1148,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Time of a tile split over a cluster that does not depend on its depth (start,
 // first round trip, sum), in ns, and of a block of K: clusters of four start
-// fastest (333 x 1000 x 1040, by 1, 2, 3, 4 CTAs: 7.1, 7.7, 7.0, 6.7 us; 300 x 512
-// x 3584, by 4, 5, 6, 8: 7.1, 7.6, 7.4, 7.3).
+// fastest (333 x 1000 x 1040, by 1, 2, 3, 4 CTAs: 7.1, 7.6, 7.0, 6.7 us; 300 x 512
+// x 3584, by 4, 5, 6, 7, 8: 7.5, 7.9, 7.9, 7.7, 7.7).  Fitted to tiles of 128
+// tokens.  The columns kernel, whose blocks take less, chooses by the same
+// figures: over 60 shapes of 1 to 64 tokens the plan took 2.4% longer than the
+// best on average.
 constexpr int64_t kBlockNs = 338;
 int64_t split_ns(int64_t blocks, int splits) {
   return (splits < 4 ? 5850 : splits == 4 ? 5600 : 6500) + kBlockNs * ceil_div(blocks, splits);
@@ -1214,17 +1225,19 @@ cudaError_t run_block_cols(const BlockLinear& l, int splits, cudaStream_t s) {
 // 4608 x 3584 takes 6.9 us instead of 6.2, 32 x 3584 x 18944 19.4 instead of 15.4).
 // Past 32, the tiles of 128 tokens start 0.7 us later but take less time for a
 // block, which pays from about 20 blocks in a row on (columns / rows, us: 33 x
-// 3584 x 3584, 7 blocks, 7.5 / 8.3; 48 x 18944 x 2048, 16, 12.4 / 13.0; 64 x 3584 x
-// 18944, 37, 19.6 / 18.0; 64 x 37888 x 3584, 56, 31 / 26).
+// 3584 x 3584, 7 blocks, 7.7 / 8.4; 48 x 18944 x 2048, 16, 12.0 / 12.1; 64 x 3584 x
+// 18944, 37, 19.7 / 18.0; 64 x 37888 x 3584, 56, 31.1 / 26.7), and, which the rule
+// does not know, for one or two blocks (64 x 5624 x 160: 5.3 / 4.0).
 //
 // More than 64 tokens: the plan with the least estimated time, in ns of a cold
 // call: a start, and for every wave of tiles the blocks of K in turn.
-// (pair / pair, K in two / tiles of 128, us: 512 x 3584 x 3584 16.4 / 14.9 /
-// 12.3; 1024 x 3584 x 3584 17.4 / 29.3 / 21.5; 512 x 3584 x 18944 67 / 43 / 50;
-// 256 x 3584 x 18944 64 / 40 / 28; 1024 x 3584 x 18944 75 / 95 / 107.)  The
-// constants are fits to 110 shapes of 65 to 4580 tokens, widths to 37888 and
-// depths to 18944; the plan chosen took 1.3% longer than the best on average, 19%
-// at most.
+// (pair / pair, K in two / tiles of 128, us: 512 x 3584 x 3584 16.5 / 14.8 /
+// 12.4; 1024 x 3584 x 3584 17.4 / 28.9 / 21.5; 512 x 3584 x 18944 64 / 41 / 52;
+// 256 x 3584 x 18944 67 / 41 / 29; 1024 x 3584 x 18944 69 / 93 / 104.)  Every plan
+// measured on 110 other shapes of 65 to 4580 tokens, widths to 37888 and depths
+// to 18944, than the constants were fitted to: the one chosen took 0.3% longer
+// than the best on average, 8% at most (up to 64 tokens, 60 shapes, 2.4% and 32%,
+// the most at 64 x 5624 x 160).
 BlockPlan plan_linear_fp8_block(int64_t M, int64_t N, int64_t K) {
   const int64_t blocks = ceil_div(K, 128);
   const int64_t columns = ceil_div(N, 128), tiles = ceil_div(M, 128) * columns;
